@@ -37,6 +37,11 @@ from ._abi import (  # noqa: F401
     hyb_attn_set_timing_events,
     hyb_attn_set_wait_limit,
     hyb_attn_set_test_flags,
+    hyb_attn_paged_cache,
+    hyb_attn_paged_batch,
+    hyb_attn_paged_append,
+    hyb_attn_paged_workspace_size,
+    hyb_attn_paged_attend,
     hyb_attn_destroy,
     hyb_attn_strerror,
     hyb_attn_last_cuda_error,
@@ -47,6 +52,13 @@ from ._abi import (  # noqa: F401
     HYB_STATUS_BAD_SELECTION,
     HYB_STATUS_TIMEOUT,
     HYB_STATUS_NAN_SCORE,
+    HYB_STATUS_BAD_PAGE,
+    HYB_STATUS_BAD_LENGTH,
+    HYB_CODE_E4M3,
+    HYB_CODE_INT8,
+    HYB_TYPE_BF16,
+    HYB_TYPE_FP16,
     HYB_TEST_WITHHOLD_SCORES,
 )
 from .layer import HybridAttentionLayer, make_config  # noqa: F401
+from .paged import PagedKVCache  # noqa: F401

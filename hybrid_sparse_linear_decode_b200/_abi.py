@@ -28,6 +28,13 @@ HYB_STATUS_DENOMINATOR = 0x2
 HYB_STATUS_BAD_SELECTION = 0x4
 HYB_STATUS_TIMEOUT = 0x8
 HYB_STATUS_NAN_SCORE = 0x10
+HYB_STATUS_BAD_PAGE = 0x20
+HYB_STATUS_BAD_LENGTH = 0x40
+
+HYB_CODE_E4M3 = 0
+HYB_CODE_INT8 = 1
+HYB_TYPE_BF16 = 0
+HYB_TYPE_FP16 = 1
 
 HYB_TEST_WITHHOLD_SCORES = 0x1
 
@@ -54,6 +61,16 @@ class hyb_attn_buffers(ctypes.Structure):
 class hyb_attn_plan_info(ctypes.Structure):
     _fields_ = [("T", c_i64), ("n_blocks", c_i64), ("k_eff", c_i64), ("exact_tokens", c_i64),
                 ("chunks_per_unit", c_i32), ("cluster_ctas", c_i32), ("grid_ctas", c_i32)]
+
+
+class hyb_attn_paged_cache(ctypes.Structure):
+    _fields_ = [("k_codes", c_vp), ("v_codes", c_vp), ("k_scales", c_vp), ("v_scales", c_vp), ("n_pages", c_i32),
+                ("n_kv_heads", c_i32), ("page_size", c_i32), ("head_dim", c_i32), ("code", c_i32)]
+
+
+class hyb_attn_paged_batch(ctypes.Structure):
+    _fields_ = [("page_table", c_vp), ("cu_new", c_vp), ("kv_lens", c_vp), ("batch", c_i32), ("table_stride", c_i32),
+                ("n_new", c_i32), ("max_new", c_i32), ("max_len", c_i32), ("status", c_vp)]
 
 
 # (name, restype, argtypes) of every entry point declared in include/hyb_attn.h
@@ -89,6 +106,14 @@ SIGNATURES = [
     ("hyb_attn_set_wait_limit", ctypes.c_int, [c_vp, ctypes.c_uint64]),
     ("hyb_attn_set_test_flags", ctypes.c_int, [c_vp, ctypes.c_uint32]),
     ("hyb_attn_destroy", None, [c_vp]),
+    ("hyb_attn_paged_append", ctypes.c_int, [ctypes.POINTER(hyb_attn_paged_cache), ctypes.POINTER(hyb_attn_paged_batch),
+                                             c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i32, c_i32, c_vp, c_i64,
+                                             c_vp, c_i64, c_i32, c_vp]),
+    ("hyb_attn_paged_workspace_size", c_sz, [ctypes.POINTER(hyb_attn_paged_cache),
+                                             ctypes.POINTER(hyb_attn_paged_batch), c_i32]),
+    ("hyb_attn_paged_attend", ctypes.c_int, [ctypes.POINTER(hyb_attn_paged_cache), ctypes.POINTER(hyb_attn_paged_batch),
+                                             c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i32, c_i32, c_f32, c_vp,
+                                             c_sz, c_vp]),
     ("hyb_attn_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("hyb_attn_last_cuda_error", ctypes.c_char_p, []),
 ]
@@ -279,3 +304,25 @@ def hyb_attn_set_test_flags(ctx: int, flags: int) -> None:
 
 def hyb_attn_destroy(ctx: int) -> None:
     load_library().hyb_attn_destroy(ctx)
+
+
+def hyb_attn_paged_append(cache: hyb_attn_paged_cache, batch: hyb_attn_paged_batch, type: int, k: int, k_stride: int,
+                          v: int, v_stride: int, rope, n_pos: int, rot_dim: int, interleaved: bool, q, q_stride: int,
+                          q_out, q_out_stride: int, n_q_heads: int, stream: int) -> None:
+    _check("hyb_attn_paged_append",
+           load_library().hyb_attn_paged_append(ctypes.byref(cache), ctypes.byref(batch), type, k, k_stride, v,
+                                                v_stride, rope, n_pos, rot_dim, interleaved, q, q_stride, q_out,
+                                                q_out_stride, n_q_heads, stream))
+
+
+def hyb_attn_paged_workspace_size(cache: hyb_attn_paged_cache, batch: hyb_attn_paged_batch, n_q_heads: int) -> int:
+    return load_library().hyb_attn_paged_workspace_size(ctypes.byref(cache), ctypes.byref(batch), n_q_heads)
+
+
+def hyb_attn_paged_attend(cache: hyb_attn_paged_cache, batch: hyb_attn_paged_batch, type: int, q: int, q_stride: int,
+                          out: int, out_stride: int, lse, n_q_heads: int, window: int, n_sink: int, scale: float,
+                          workspace, workspace_bytes: int, stream: int) -> None:
+    _check("hyb_attn_paged_attend",
+           load_library().hyb_attn_paged_attend(ctypes.byref(cache), ctypes.byref(batch), type, q, q_stride, out,
+                                                out_stride, lse, n_q_heads, window, n_sink, scale, workspace,
+                                                workspace_bytes, stream))

@@ -139,6 +139,12 @@ int cuda_fail(cudaError_t e) {
   return HYB_ECUDA;
 }
 
+}  // namespace
+
+int hyb::record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+namespace {
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

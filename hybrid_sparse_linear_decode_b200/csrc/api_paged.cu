@@ -1,0 +1,185 @@
+// C ABI of the paged 8-bit cache: argument checks, work splits, launches.  Host code only.
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "hyb_internal.h"
+#include "k_paged.h"
+
+using namespace hyb;
+
+namespace {
+
+// The splits are planned for this many SMs; a device with fewer still runs them.
+constexpr int kSms = 148;
+
+bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+};
+
+// Shapes only (what the workspace size depends on).
+bool shapes_ok(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b) {
+  if (c == nullptr || b == nullptr) return false;
+  if (c->n_pages < 1 || c->n_kv_heads < 1) return false;
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  if (c->page_size < 16 || c->page_size > 256 || c->page_size % 16 != 0) return false;
+  if (c->code != HYB_CODE_E4M3 && c->code != HYB_CODE_INT8) return false;
+  if (b->batch < 1 || b->table_stride < 1 || (int64_t)b->table_stride * c->page_size > ((int64_t)1 << 30)) return false;
+  if ((int64_t)b->batch * c->n_kv_heads > 65535) return false;
+  if (b->n_new < 0 || b->n_new > (1 << 30) || b->max_new < 0 || b->max_new > b->n_new || b->max_len < 0) return false;
+  return b->n_new == 0 || b->max_new > 0;
+}
+
+bool pointers_ok(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b) {
+  return aligned(c->k_codes, 16) && aligned(c->v_codes, 16) && aligned(c->k_scales, 4) && aligned(c->v_scales, 4) &&
+         aligned(b->page_table, 4) && aligned(b->cu_new, 4) && aligned(b->kv_lens, 4) &&
+         (b->status == nullptr || aligned(b->status, 4));
+}
+
+PagedCache cache_of(const hyb_attn_paged_cache* c) {
+  return PagedCache{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes), c->k_scales, c->v_scales,
+                    c->n_pages, c->n_kv_heads, c->page_size};
+}
+PagedBatch batch_of(const hyb_attn_paged_batch* b) {
+  return PagedBatch{b->page_table, b->cu_new, b->kv_lens, b->batch, b->table_stride, b->n_new, b->max_new};
+}
+
+// Rows of `heads` heads of head_dim elements, `stride` elements apart.
+bool rows_ok(const void* p, int64_t stride, int64_t heads, int d, int64_t unit) {
+  return aligned(p, unit * 2) && stride % unit == 0 && stride >= heads * d && stride < ((int64_t)1 << 40);
+}
+
+struct Plan {
+  int tiles;     // 16-row tiles of the narrow form; 0 selects the wide form
+  int n_cta;     // narrow
+  int n_splits;  // wide
+  size_t bytes;
+};
+
+// Narrow up to 32 rows a KV head: two row tiles share one conversion of the codes, and more do not fit the
+// registers.  Every CTA gets at least a stage for each of its warps, at most two CTAs an SM.
+// Wide: as many parts of each row tile's stages as fill the SMs, each of at least 8 stages.
+Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink) {
+  Plan p{};
+  const int G = Hq / c->n_kv_heads;
+  const int64_t units = (int64_t)b->batch * c->n_kv_heads;
+  const int64_t rows = (int64_t)b->max_new * G;
+  int64_t len = std::min<int64_t>(b->max_len, (int64_t)b->table_stride * c->page_size);
+  if (window > 0) len = std::min<int64_t>(len, (int64_t)window + sink + b->max_new + 64);
+  const int64_t stages = std::max<int64_t>(1, (len + 31) / 32);
+  const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
+  if (rows <= kNarrowRows) {
+    p.tiles = rows <= 16 ? 1 : 2;
+    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * kPagedCtasPerSm, (units * stages + 3) / 4));
+    p.bytes = (size_t)2 * p.n_cta * 16 * p.tiles * row_bytes;
+  } else {
+    const int64_t tiles = units * ((rows + kWideRows - 1) / kWideRows);
+    int64_t n = tiles >= kSms * kPagedCtasPerSm ? 1 : (kSms * kPagedCtasPerSm + tiles - 1) / tiles;
+    n = std::max<int64_t>(1, std::min<int64_t>({n, stages / 8, 64}));
+    if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
+    p.n_splits = (int)n;
+    p.bytes = n > 1 ? (size_t)n * b->n_new * Hq * row_bytes : 0;
+  }
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hyb_attn_paged_append(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* rope,
+                          int32_t n_pos, int32_t rot_dim, int32_t interleaved, const void* q, int64_t q_stride,
+                          void* q_out, int64_t q_out_stride, int32_t n_q_heads, cudaStream_t stream) {
+  const NvtxRange range(__func__);
+  if (!shapes_ok(cache, batch) || !pointers_ok(cache, batch)) return HYB_EINVAL;
+  if (type != HYB_TYPE_BF16 && type != HYB_TYPE_FP16) return HYB_EINVAL;
+  const int d = cache->head_dim;
+  if ((q == nullptr) != (q_out == nullptr)) return HYB_EINVAL;
+  if (rope != nullptr && (!aligned(rope, 16) || n_pos < 1 || rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0))
+    return HYB_EINVAL;
+  if (batch->n_new == 0) return HYB_OK;
+  if (!rows_ok(k, k_stride, cache->n_kv_heads, d, 8) || !rows_ok(v, v_stride, cache->n_kv_heads, d, 8)) return HYB_EINVAL;
+  if (q != nullptr) {
+    if (n_q_heads < 1 || !rows_ok(q, q_stride, n_q_heads, d, 8) || !rows_ok(q_out, q_out_stride, n_q_heads, d, 8))
+      return HYB_EINVAL;
+    if (q == q_out && q_stride != q_out_stride) return HYB_EINVAL;
+  }
+  PagedAppendParams p{};
+  p.c = cache_of(cache);
+  p.b = batch_of(batch);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.rope = rope;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_stride = q_stride;
+  p.qo_stride = q_out_stride;
+  p.Hq = q != nullptr ? n_q_heads : 0;
+  p.D = d;
+  p.rot = rope != nullptr ? rot_dim : 0;
+  p.n_pos = n_pos;
+  p.int8 = cache->code == HYB_CODE_INT8;
+  p.half = type == HYB_TYPE_FP16;
+  p.interleaved = interleaved != 0;
+  p.pages_max = (batch->max_new - 1 + cache->page_size - 1) / cache->page_size + 1;
+  p.kv_blocks = (int64_t)batch->batch * p.pages_max * cache->n_kv_heads * 2;
+  p.status = batch->status;
+  if (p.kv_blocks + (int64_t)batch->n_new * (p.Hq + 3) / 4 * 8 / 32 + 1 >= ((int64_t)1 << 31)) return HYB_EINVAL;
+  const cudaError_t e = launch_paged_append(p, stream);
+  return e == cudaSuccess ? HYB_OK : record_cuda_error(e);
+}
+
+size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch,
+                                     int32_t n_q_heads) {
+  if (!shapes_ok(cache, batch) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || batch->n_new == 0) return 0;
+  return make_plan(cache, batch, n_q_heads, 0, 0).bytes;
+}
+
+int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
+                          const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
+                          int32_t n_q_heads, int32_t window, int32_t n_sink, float scale, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  const NvtxRange range(__func__);
+  if (!shapes_ok(cache, batch) || !pointers_ok(cache, batch)) return HYB_EINVAL;
+  if (type != HYB_TYPE_BF16 && type != HYB_TYPE_FP16) return HYB_EINVAL;
+  if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0) return HYB_EINVAL;
+  if (window < 0 || n_sink < 0 || !(scale >= 0.f) || !std::isfinite(scale)) return HYB_EINVAL;
+  const int d = cache->head_dim;
+  if (batch->n_new == 0) return HYB_OK;
+  if (!rows_ok(q, q_stride, n_q_heads, d, 8) || !rows_ok(out, out_stride, n_q_heads, d, 4)) return HYB_EINVAL;
+  if (lse != nullptr && !aligned(lse, 4)) return HYB_EINVAL;
+  if ((int64_t)batch->max_new * (n_q_heads / cache->n_kv_heads) > ((int64_t)1 << 30)) return HYB_EINVAL;
+  const Plan plan = make_plan(cache, batch, n_q_heads, window, n_sink);
+  if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes)) return HYB_ESCRATCH;
+  if (plan.bytes > 0 && !aligned(workspace, 16)) return HYB_EINVAL;
+  PagedAttnParams p{};
+  p.c = cache_of(cache);
+  p.b = batch_of(batch);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.Hq = n_q_heads;
+  p.G = n_q_heads / cache->n_kv_heads;
+  p.half = type == HYB_TYPE_FP16;
+  p.W = window;
+  p.S = window > 0 ? n_sink : 0;
+  p.scale = (scale > 0.f ? scale : 1.f / sqrtf((float)d)) * 1.44269504088896341f;
+  p.n_cta = plan.n_cta;
+  p.n_splits = plan.n_splits;
+  p.ws = static_cast<float*>(workspace);
+  p.status = batch->status;
+  const int int8 = cache->code == HYB_CODE_INT8;
+  const cudaError_t e = plan.tiles > 0 ? launch_paged_narrow(p, d, int8, plan.tiles, stream) : launch_paged_wide(p, d, int8, stream);
+  return e == cudaSuccess ? HYB_OK : record_cuda_error(e);
+}
+
+}  // extern "C"

@@ -73,6 +73,9 @@ extern "C" {
 #define HYB_STATUS_BAD_SELECTION 0x4u  /* a caller-given block index was out of range (skipped) */
 #define HYB_STATUS_TIMEOUT       0x8u  /* a bounded wait inside a kernel gave up */
 #define HYB_STATUS_NAN_SCORE     0x10u /* a block score was NaN (ranked last) */
+/* bits of the caller's own status word (paged cache calls) */
+#define HYB_STATUS_BAD_PAGE      0x20u /* a page index outside the cache (its tokens are skipped) */
+#define HYB_STATUS_BAD_LENGTH    0x40u /* lengths or row ranges outside what the call was told (held to it) */
 
 /* ---- failure injection for tests (hyb_attn_set_test_flags) ---------------- */
 #define HYB_TEST_WITHHOLD_SCORES 0x1u  /* rank 1 of every unit's cluster does not hand its block
@@ -407,6 +410,111 @@ const char* hyb_attn_last_cuda_error(void);
 
 /* Static description of a return code. */
 const char* hyb_attn_strerror(int code);
+
+/* ===========================================================================
+ * Paged 8-bit cache: append with rotation, attention
+ *
+ * The caches above hold each batch row's history in one run of bf16 rows.  A
+ * layer that keeps full attention (or sinks and a window only) beside them can
+ * keep its history in pages of 8-bit codes instead.  These calls have no
+ * context: everything is in their arguments, the caller owns every buffer, and
+ * a call reads and writes only what it is given, so it can be captured into a
+ * CUDA graph.  Lengths and page tables are device arrays (a captured call sees
+ * their current values); the host gives upper limits.
+ *
+ * A value is code * scale, with one scale per page and KV head, for keys and
+ * values apart.  e4m3 codes: the scale is the smallest power of two (2^-126 ..
+ * 2^126) with |x| <= 448 * scale for all x of the page; int8 codes: the largest
+ * |x| / 127 (2^-126 at least).
+ * ======================================================================== */
+#define HYB_CODE_E4M3 0
+#define HYB_CODE_INT8 1
+#define HYB_TYPE_BF16 0
+#define HYB_TYPE_FP16 1
+
+/* One layer's cache.  Codes [n_pages][n_kv_heads][page_size][head_dim], scales
+ * fp32 [n_pages][n_kv_heads].  head_dim 64 or 128; page_size a multiple of 16,
+ * at most 256; code pointers 16-byte aligned, scales 4-byte.  Pages never
+ * written need no initial value. */
+typedef struct hyb_attn_paged_cache {
+  void*  k_codes;
+  void*  v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t n_pages;
+  int32_t n_kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t code;        /* HYB_CODE_* */
+} hyb_attn_paged_cache;
+
+/* The sequences of one step, in device arrays.  Sequence b owns rows
+ * [cu_new[b], cu_new[b + 1]) of the step's token rows, and has kv_lens[b] tokens
+ * once these are counted: its new tokens are the last ones, at positions
+ * kv_lens[b] - (cu_new[b + 1] - cu_new[b]) and up.  Tokens [i * page_size,
+ * (i + 1) * page_size) lie in page page_table[b * table_stride + i].  Rows
+ * behind cu_new[batch] are left as they were.  Sequences may share pages that
+ * this step only reads; a page that it appends to belongs to one sequence.
+ * Values that contradict the limits (or each other) are held to them and set
+ * HYB_STATUS_BAD_LENGTH; tokens on pages outside the cache are not written, or
+ * not seen, and set HYB_STATUS_BAD_PAGE. */
+typedef struct hyb_attn_paged_batch {
+  const int32_t* page_table;  /* [batch][table_stride] */
+  const int32_t* cu_new;      /* [batch + 1], rising, from 0 to at most n_new */
+  const int32_t* kv_lens;     /* [batch] */
+  int32_t batch;              /* >= 1 */
+  int32_t table_stride;       /* pages of a table row; table_stride * page_size <= 2^30 */
+  int32_t n_new;              /* token rows of the step's arrays */
+  int32_t max_new;            /* most new tokens of one sequence, <= n_new */
+  int32_t max_len;            /* most tokens of one sequence (plans the split only) */
+  uint32_t* status;           /* device word that HYB_STATUS_* bits are added to, or NULL */
+} hyb_attn_paged_batch;
+
+/* Append the new tokens of a step, keys rotated by their position, and give
+ * the queries rotated alike:
+ *   k, v   bf16 or fp16 (`type`) [n_new] rows of [n_kv_heads][head_dim], rows
+ *          k_stride / v_stride elements apart (a multiple of 8)
+ *   rope   fp32 [n_pos][rot_dim]: each position's rot_dim / 2 cosines, then its
+ *          sines; NULL for no rotation.  rot_dim a multiple of 16, at most
+ *          head_dim; channels past it are left alone.  Pair i is channels
+ *          (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `interleaved`:
+ *          (a, b) -> (a cos - b sin, b cos + a sin).
+ *   q      [n_new] rows of [n_q_heads][head_dim], to q_out in the same type; may
+ *          be the same rows; both NULL for none.
+ * A page that the new tokens begin gets the scale that they need.  A page that
+ * already holds tokens of the sequence keeps its scale unless a new token needs a
+ * larger one; its codes are then rewritten once for the new scale.  Codes are
+ * the nearest (ties to even) to x / scale.  A NaN is stored as 0 and an infinity as the
+ * largest code, both without effect on the scale, and set
+ * HYB_STATUS_NONFINITE.  Appending the same tokens again gives the same cache.
+ * A position at or past n_pos takes the last one's angles and sets
+ * HYB_STATUS_BAD_LENGTH.  One launch.  Errors: HYB_EINVAL, HYB_ECUDA. */
+int hyb_attn_paged_append(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* rope,
+                          int32_t n_pos, int32_t rot_dim, int32_t interleaved, const void* q, int64_t q_stride,
+                          void* q_out, int64_t q_out_stride, int32_t n_q_heads, cudaStream_t stream);
+
+/* Workspace bytes of hyb_attn_paged_attend for these limits (0 when it refuses
+ * them).  Host only. */
+size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch,
+                                     int32_t n_q_heads);
+
+/* Causal attention of a step's new tokens over the cache (which holds them
+ * already): row i at position t sees positions j <= t and, with window W > 0,
+ * only j > t - W or j < n_sink.  o = sum softmax(scale q . k_j) v_j, query head i
+ * on KV head i / (n_q_heads / n_kv_heads).
+ *   q      bf16 or fp16 [n_new] rows of [n_q_heads][head_dim], q_stride apart (a
+ *          multiple of 8);  out: the same type, out_stride apart (a multiple of 4)
+ *   lse    fp32 [n_new][n_q_heads]: log of the sum of exp(scale q . k_j); or NULL
+ * A row that sees nothing gets zeros and lse = -inf.  scale 0 selects
+ * 1/sqrt(head_dim).  Values are as if in 32 bits but for the softmax weights,
+ * which are rounded to 11 bits.  The workspace (16-byte aligned) holds nothing
+ * between calls; calls that may run at the same time need one each.
+ * Errors: HYB_EINVAL, HYB_ESCRATCH (workspace too small), HYB_ECUDA. */
+int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
+                          const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
+                          int32_t n_q_heads, int32_t window, int32_t n_sink, float scale, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -61,7 +61,7 @@ struct Plan {
 };
 
 // Narrow up to 32 rows a KV head: two row tiles share one conversion of the codes, and more do not fit the
-// registers.  Every CTA gets at least a stage for each of its warps, at most two CTAs an SM.
+// registers.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
 // Wide: as many parts of each row tile's stages as fill the SMs, each of at least 8 stages.
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink) {
   Plan p{};
@@ -74,11 +74,11 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
   if (rows <= kNarrowRows) {
     p.tiles = rows <= 16 ? 1 : 2;
-    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * kPagedCtasPerSm, (units * stages + 3) / 4));
+    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * narrow_ctas_per_sm(p.tiles), (units * stages + 3) / 4));
     p.bytes = (size_t)2 * p.n_cta * 16 * p.tiles * row_bytes;
   } else {
     const int64_t tiles = units * ((rows + kWideRows - 1) / kWideRows);
-    int64_t n = tiles >= kSms * kPagedCtasPerSm ? 1 : (kSms * kPagedCtasPerSm + tiles - 1) / tiles;
+    int64_t n = tiles >= kSms * kWideCtasPerSm ? 1 : (kSms * kWideCtasPerSm + tiles - 1) / tiles;
     n = std::max<int64_t>(1, std::min<int64_t>({n, stages / 8, 64}));
     if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
     p.n_splits = (int)n;

@@ -327,7 +327,12 @@ constexpr int kWarps = 4;
 template <int D>
 struct StageGeo {
   static constexpr int kBytes = kStageTokens * D * 2 + 32;  // K codes, V codes, scales and flags
-  static constexpr int kStages = D == 128 ? 3 : 5;          // of each warp's ring (narrow form)
+};
+// Narrow form: CTAs an SM (registers: 168 or 255 a thread) and stages of each warp's ring.
+template <int D, int MT>
+struct NarrowGeo {
+  static constexpr int kCtas = narrow_ctas_per_sm(MT);
+  static constexpr int kStages = D == 128 ? (MT == 1 ? 2 : 3) : (MT == 1 ? 4 : 5);
 };
 
 // 16-byte column of a stage row, moved so that the reads of both products meet
@@ -779,9 +784,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m - 15.f + log2f(l)) * kLn2; }
 
 template <int D, bool INT8, int MT>
-__global__ void __launch_bounds__(kWarps * 32, kPagedCtasPerSm) paged_narrow_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, MT>::kCtas) paged_narrow_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kRing = StageGeo<D>::kStages, kBytes = StageGeo<D>::kBytes;
+  constexpr int kRing = NarrowGeo<D, MT>::kStages, kBytes = StageGeo<D>::kBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kRing * kBytes;
   uint4* qf = reinterpret_cast<uint4*>(smem + kWarps * kRing * kBytes);
@@ -909,23 +914,88 @@ __global__ void __launch_bounds__(kWarps * 32, kPagedCtasPerSm) paged_narrow_ker
   }
 }
 
+// Joins n parts of a row: `part(i)` is the i-th part's [D outputs, m, l].  kJoinThreads threads; returns the four
+// channels 4 c .. of thread c < D / 4, the row's maximum and sum.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinMost = 512;  // parts
+
+template <int D, class F>
+__device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& sum) {
+  __shared__ float weight[kJoinMost], red[2][kJoinThreads / 32];
+  __shared__ float4 acc[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, part(i)[D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[0][tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
+  float l = 0.f;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float* e = part(i);
+    const float w = m == -INFINITY ? 0.f : exp2f(e[D] - m) * e[D + 1];
+    weight[i] = w;
+    l += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[1][tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
+  // D / 4 threads a part
+  constexpr int kSide = kJoinThreads / (D / 4);
+  const int c = tid % (D / 4), first = tid / (D / 4);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = first; i < n; i += kSide) {
+    const float w = weight[i];
+    const float4 o = *reinterpret_cast<const float4*>(part(i) + 4 * c);
+    y.x += w * o.x, y.y += w * o.y, y.z += w * o.z, y.w += w * o.w;
+  }
+  acc[tid] = y;
+  __syncthreads();
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int g = 0; g < kSide; ++g) {
+    const float4 o = acc[g * (D / 4) + c];
+    y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+  }
+  y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+  top = m;
+  sum = l;
+  return y;
+}
+
+__device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t tok, int hd, int D, int c, const float4& y,
+                                             float m, float l) {
+  *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + 4 * c) =
+      make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
+  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+}
+
 // Joins the parts of units that more than one CTA worked on, and writes the rows
-// of units with no visible token.  One CTA a (unit, row), a thread a channel.
+// of units with no visible token.  One CTA a (unit, row).
 template <int D>
-__global__ void __launch_bounds__(D) paged_join_kernel(const PagedAttnParams p, int tile_rows) {
-  pdl_wait_primary();
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnParams p, int tile_rows) {
   const int unit = blockIdx.x, row = blockIdx.y;
   const int b = unit / p.c.Hkv, h = unit % p.c.Hkv;
   bool bad;
   const Seq seq = read_seq(p.b, b, p.c.P, &bad);
-  if (row >= min(seq.n * p.G, tile_rows)) return;
+  if (row >= min(seq.n * p.G, tile_rows)) {
+    pdl_wait_primary();  // every block: this grid's end stands for the attention's too
+    return;
+  }
   const int64_t tok = seq.t0 + row / p.G;
-  const int hd = h * p.G + row % p.G, c = threadIdx.x;
+  const int hd = h * p.G + row % p.G;
   const int stages = seq_span(p, seq).stages;
-  uint16_t* out = p.out + tok * p.out_stride + (int64_t)hd * D + c;
   if (stages == 0) {
-    *out = 0;
-    if (c == 0) store_row(p, tok, hd, -INFINITY);
+    pdl_wait_primary();
+    if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
     return;
   }
   // the line up to this sequence
@@ -943,26 +1013,23 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const PagedAttnParams p, 
   }
   total *= p.c.Hkv;
   const int64_t begin = before * p.c.Hkv + (int64_t)h * stages, endu = begin + stages;
-  // the CTA c whose part [total c / n, total (c + 1) / n) holds a stage x is ceil((x + 1) n / total) - 1
+  // the CTA whose part [total c / n, total (c + 1) / n) holds a stage x is c = ceil((x + 1) n / total) - 1;
+  // with fewer stages than CTAs the parts are of one stage or none, and those in between that have none are passed over
   const int c0 = (int)(((begin + 1) * p.n_cta + total - 1) / total) - 1;
   const int c1 = (int)((endu * p.n_cta + total - 1) / total) - 1;
+  pdl_wait_primary();
   if (c0 == c1) return;  // complete in one CTA
-  float m = -INFINITY, l = 0.f, y = 0.f;
-  for (int i = c0; i <= c1; ++i) {
-    const int slot = 2 * i + (cut(total, p.n_cta, i) < begin ? 1 : 0);
-    const float* ws = p.ws + ((int64_t)slot * tile_rows + row) * (D + 4);
-    if (cut(total, p.n_cta, i) == cut(total, p.n_cta, i + 1)) continue;  // an empty part
-    const float mi = ws[D], li = ws[D + 1], oi = ws[c];
-    const float mn = fmaxf(m, mi);
-    if (mn == -INFINITY) continue;
-    const float a = exp2f(m - mn), w = exp2f(mi - mn) * li;
-    l = l * a + w;
-    y = y * a + oi * w;
-    m = mn;
-  }
-  y = l == 0.f ? 0.f : y / l;
-  *out = (uint16_t)(pack_out(y, 0.f, p.half) & 0xffffu);
-  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+  const bool sparse = total < p.n_cta;
+  const int n = sparse ? stages : c1 - c0 + 1;
+  const bool starts_before = cut(total, p.n_cta, c0) < begin;
+  auto part = [&](int i) -> const float* {
+    const int c = sparse ? (int)(((begin + i + 1) * p.n_cta + total - 1) / total) - 1 : c0 + i;
+    const int64_t slot = 2 * (int64_t)c + (i == 0 && starts_before ? 1 : 0);
+    return p.ws + (slot * tile_rows + row) * (D + 4);
+  };
+  float m, l;
+  const float4 y = join_parts<D>(n, part, m, l);
+  if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, y, m, l);
 }
 
 // ---- the wide form: many rows a KV head --------------------------------------------------------------
@@ -975,7 +1042,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const PagedAttnParams p, 
 constexpr int kWideRing = 4;
 
 template <int D, bool INT8>
-__global__ void __launch_bounds__(kWarps * 32, kPagedCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int MT = 2, kBytes = StageGeo<D>::kBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -1072,27 +1139,17 @@ __global__ void __launch_bounds__(kWarps * 32, kPagedCtasPerSm) paged_wide_kerne
 }
 
 template <int D>
-__global__ void __launch_bounds__(D) paged_join_rows_kernel(const PagedAttnParams p) {
-  pdl_wait_primary();
+__global__ void __launch_bounds__(kJoinThreads) paged_join_rows_kernel(const PagedAttnParams p) {
   bool bad;
   const Seq seq = read_seq(p.b, blockIdx.z, p.c.P, &bad);
+  pdl_wait_primary();
   if ((int)blockIdx.y >= seq.n) return;
   const int64_t tok = seq.t0 + blockIdx.y;
-  const int hd = blockIdx.x, c = threadIdx.x;
-  float m = -INFINITY, l = 0.f, y = 0.f;
-  for (int i = 0; i < p.n_splits; ++i) {
-    const float* ws = p.ws + (((int64_t)i * p.b.n_new + tok) * p.Hq + hd) * (D + 4);
-    const float mi = ws[D], li = ws[D + 1], oi = ws[c];
-    const float mn = fmaxf(m, mi);
-    if (mn == -INFINITY) continue;
-    const float a = exp2f(m - mn), w = exp2f(mi - mn) * li;
-    l = l * a + w;
-    y = y * a + oi * w;
-    m = mn;
-  }
-  y = l == 0.f ? 0.f : y / l;
-  p.out[tok * p.out_stride + (int64_t)hd * D + c] = (uint16_t)(pack_out(y, 0.f, p.half) & 0xffffu);
-  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+  const int hd = blockIdx.x;
+  auto part = [&](int i) -> const float* { return p.ws + (((int64_t)i * p.b.n_new + tok) * p.Hq + hd) * (D + 4); };
+  float m, l;
+  const float4 y = join_parts<D>(p.n_splits, part, m, l);
+  if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, y, m, l);
 }
 
 // ---- launches -----------------------------------------------------------------------------------------
@@ -1117,14 +1174,14 @@ cudaError_t launch(void (*f)(A...), dim3 grid, dim3 block, size_t smem, bool cha
 
 template <int D, bool INT8, int MT>
 cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
-  constexpr size_t rings = (size_t)kWarps * StageGeo<D>::kStages * StageGeo<D>::kBytes;
+  constexpr size_t rings = (size_t)kWarps * NarrowGeo<D, MT>::kStages * StageGeo<D>::kBytes;
   constexpr size_t frags = (size_t)MT * (D / 16) * 32 * sizeof(uint4);
   static_assert(rings >= (size_t)kWarps * 16 * MT * D * sizeof(float), "the join's rows fit the rings");
   static_assert(frags >= (size_t)kWarps * 16 * MT * 3 * sizeof(float), "the join's sums fit the fragments");
   cudaError_t e = launch(paged_narrow_kernel<D, INT8, MT>, dim3(p.n_cta), dim3(kWarps * 32), rings + frags, false, s, p);
   if (e != cudaSuccess) return e;
   const int rows = p.b.max_new * p.G < 16 * MT ? p.b.max_new * p.G : 16 * MT;
-  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, rows), dim3(D), 0, true, s, p, 16 * MT);
+  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, rows), dim3(kJoinThreads), 0, true, s, p, 16 * MT);
 }
 
 template <int D, bool INT8>
@@ -1137,7 +1194,7 @@ cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   cudaError_t e = launch(paged_wide_kernel<D, INT8>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
                          dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(D), 0, true, s, p);
+  return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(kJoinThreads), 0, true, s, p);
 }
 
 }  // namespace

@@ -59,7 +59,8 @@ struct PagedAttnParams {
 // narrow form takes: two 16-row matrix tiles.
 constexpr int kNarrowRows = 32;
 constexpr int kWideRows = 128;  // rows of a CTA of the wide form
-constexpr int kPagedCtasPerSm = 2;
+constexpr int kWideCtasPerSm = 2;
+constexpr int narrow_ctas_per_sm(int tiles) { return tiles == 1 ? 3 : 2; }
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int tiles, cudaStream_t s);

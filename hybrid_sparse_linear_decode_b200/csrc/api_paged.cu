@@ -30,6 +30,8 @@ bool shapes_ok(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b) {
   if (c->code != HYB_CODE_E4M3 && c->code != HYB_CODE_INT8) return false;
   if (b->batch < 1 || b->table_stride < 1 || (int64_t)b->table_stride * c->page_size > ((int64_t)1 << 30)) return false;
   if ((int64_t)b->batch * c->n_kv_heads > 65535) return false;
+  // 32-token stages of all sequences and KV heads are counted in 31 bits
+  if ((int64_t)b->batch * c->n_kv_heads * ((int64_t)b->table_stride * c->page_size / 32 + 2) >= ((int64_t)1 << 31)) return false;
   if (b->n_new < 0 || b->n_new > (1 << 30) || b->max_new < 0 || b->max_new > b->n_new || b->max_len < 0) return false;
   return b->n_new == 0 || b->max_new > 0;
 }
@@ -54,14 +56,14 @@ bool rows_ok(const void* p, int64_t stride, int64_t heads, int d, int64_t unit) 
 }
 
 struct Plan {
-  int tiles;     // 16-row tiles of the narrow form; 0 selects the wide form
+  int tiles;     // 8-row tiles of the narrow form (1, 2 or 4); 0 selects the wide form
   int n_cta;     // narrow
   int n_splits;  // wide
   size_t bytes;
 };
 
-// Narrow up to 32 rows a KV head: two row tiles share one conversion of the codes, and more do not fit the
-// registers.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
+// Narrow up to 32 rows a KV head: the row tiles share one conversion of the codes, and more than four do not fit
+// the registers.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
 // Wide: as many parts of each row tile's stages as fill the SMs, each of at least 8 stages.
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink) {
   Plan p{};
@@ -73,9 +75,9 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   const int64_t stages = std::max<int64_t>(1, (len + 31) / 32);
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
   if (rows <= kNarrowRows) {
-    p.tiles = rows <= 16 ? 1 : 2;
+    p.tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * narrow_ctas_per_sm(p.tiles), (units * stages + 3) / 4));
-    p.bytes = (size_t)2 * p.n_cta * 16 * p.tiles * row_bytes;
+    p.bytes = (size_t)2 * p.n_cta * 8 * p.tiles * row_bytes;
   } else {
     const int64_t tiles = units * ((rows + kWideRows - 1) / kWideRows);
     int64_t n = tiles >= kSms * kWideCtasPerSm ? 1 : (kSms * kWideCtasPerSm + tiles - 1) / tiles;

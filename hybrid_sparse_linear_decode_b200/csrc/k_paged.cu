@@ -316,10 +316,14 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
 // 11 bits down to 2^-29 of the largest, which is one rounding of 2^-12 a weight,
 // below the output type's own.  All sums are in 32 bits.
 //
-// Matrix form (mma.m16n8k16): S = Q C_k^T with 16 rows of queries and 8 tokens,
-// O = P C_v.  The channel and token orders inside a k-step are free as long as
-// both operands agree, so a lane reads its 16 bytes of a token's codes at once
-// and each 4-byte word of them is one k-step's fragment after two conversions.
+// Matrix form (mma.m16n8k16), with 8 query rows as the narrow side so that the few
+// rows of a decode step fill it: S^T = C_k Q^T with 16 tokens by 8 rows, O^T = C_v^T P^T
+// with 16 channels by 8 rows.  The channel order inside a k-step of the first product is
+// free as long as both operands agree, and so is the order of the second product's
+// output rows: a lane reads 16 bytes of a token's codes at once, each 4-byte word of a
+// key is one k-step's fragment after two conversions, and the words of two
+// tokens' values, their bytes interleaved, are fragments of the second product.  The
+// weights get from the first product's layout to the second's by 8 x 8 transposes.
 
 constexpr int kStageTokens = 32;
 constexpr int kWarps = 4;
@@ -329,10 +333,10 @@ struct StageGeo {
   static constexpr int kBytes = kStageTokens * D * 2 + 32;  // K codes, V codes, scales and flags
 };
 // Narrow form: CTAs an SM (registers: 168 or 255 a thread) and stages of each warp's ring.
-template <int D, int MT>
+template <int D, int NT>
 struct NarrowGeo {
-  static constexpr int kCtas = narrow_ctas_per_sm(MT);
-  static constexpr int kStages = D == 128 ? (MT == 1 ? 2 : 3) : (MT == 1 ? 4 : 5);
+  static constexpr int kCtas = narrow_ctas_per_sm(NT);
+  static constexpr int kStages = D == 128 ? (kCtas == 3 ? 2 : 3) : (kCtas == 3 ? 4 : 5);
 };
 
 // 16-byte column of a stage row, moved so that the reads of both products meet
@@ -482,41 +486,63 @@ __device__ __forceinline__ void issue_stage(const PagedAttnParams& p, uint8_t* s
   }
 }
 
-// A warp's rows: MT tiles of 16; this lane's are g and g + 8 of each (g = lane / 4).
-template <int D, int MT>
+// A warp's rows: NT tiles of 8; this lane's are columns 2 t and 2 t + 1 of each (t = lane % 4).
+template <int D, int NT>
 struct Rows {
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2], rf[MT][2];
-  int pos[MT][2];     // position, or -1 for a row that is not there
-  uint32_t ref;       // exponent field of the value scales' reference
+  float o[NT][D / 16][4];  // channels (D / 8) g + 2 j (elements 0, 1) and the next (2, 3), g = lane / 4
+  float m[NT][2], l[NT][2], rf[NT][2];
+  int pos[NT][2];        // position, or -1 for a row that is not there
+  uint32_t ref;          // exponent field of the value scales' reference
   int pos_min, pos_max;  // of the warp's rows that are there
 
   __device__ __forceinline__ void clear() {
     ref = 1;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-      m[t][0] = m[t][1] = -INFINITY;
-      l[t][0] = l[t][1] = 0.f;
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
     }
   }
 };
 
-// Fragments of 16 query rows in shared memory: for each k-step and lane the four registers of the A operand.
-// The lane holding row g reads channels 16 t + 4 s .. + 3 (and 64 more for the upper half of D = 128) of rows g
-// and g + 8; every warp gets its rows' factors, those with `write` store the fragments.
-template <int D>
-__device__ __forceinline__ void load_q_tile(const PagedAttnParams& p, uint4* frag, int t0, int h, int row_first,
-                                            int rows, float* rf, bool write) {
+// Query fragments of NT row tiles: for k-step s, channels 16 t + 4 s .. + 3 (64 more for the upper half of D = 128)
+// of row g.  Up to 16 rows stay in registers, 32 rows go through shared memory (in pairs of tiles, [s][pair][lane]).
+template <int D, int NT>
+struct Queries {
+  static constexpr bool kRegs = NT <= 2;
+  uint2 reg[kRegs ? NT : 1][kRegs ? D / 16 : 1];
+  const uint4* mem;
+
+  __device__ __forceinline__ void get(int s, uint2 (&q)[NT]) const {
+    if (kRegs) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) q[n] = reg[kRegs ? n : 0][kRegs ? s : 0];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        const uint4 x = mem[(s * (NT / 2) + n / 2) * 32 + (threadIdx.x & 31)];
+        q[n] = make_uint2(x.x, x.y);
+        q[n + 1 < NT ? n + 1 : n] = make_uint2(x.z, x.w);
+      }
+    }
+  }
+};
+
+// Loads the fragments of rows row_first .. and the rows' factors and positions.  `mem` (32 rows only): where the
+// fragments go; of the warps that share it those with `write` store them.
+template <int D, int NT>
+__device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, NT>& Q, Rows<D, NT>& R, uint4* mem,
+                                          int t0, int h, int row_first, int rows, int pos0, bool write) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool half = p.half != 0;
-  uint32_t a[2][D / 16][2];
+  uint2 frag[NT][D / 16];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = row_first + g + 8 * r;
+  for (int n = 0; n < NT; ++n) {
+    const int row = row_first + 8 * n + g;
     const bool there = row < rows;
     const int tok = there ? row / p.G : 0, head = there ? row % p.G : 0;
     const uint16_t* src = p.q + (int64_t)(t0 + tok) * p.q_stride + (int64_t)(h * p.G + head) * D + 16 * t;
@@ -541,147 +567,170 @@ __device__ __forceinline__ void load_q_tile(const PagedAttnParams& p, uint4* fra
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
     const float inv = pow2_of(254u - e);
-    rf[r] = pow2_of(e) * p.scale;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const float* y = x[s >> 2] + 4 * (s & 3);
-      a[r][s][0] = pack_half(y[0] * inv, y[1] * inv);
-      a[r][s][1] = pack_half(y[2] * inv, y[3] * inv);
+      frag[n][s] = make_uint2(pack_half(y[0] * inv, y[1] * inv), pack_half(y[2] * inv, y[3] * inv));
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      R.rf[n][c] = pow2_of(__shfl_sync(0xffffffffu, e, (2 * t + c) * 4)) * p.scale;
+      const int r = row_first + 8 * n + 2 * t + c;
+      R.pos[n][c] = r < rows ? pos0 + r / p.G : -1;
     }
   }
-  if (!write) return;
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) frag[s * 32 + lane] = make_uint4(a[0][s][0], a[1][s][0], a[0][s][1], a[1][s][1]);
-}
-
-template <int D, int MT>
-__device__ __forceinline__ void set_rows(const PagedAttnParams& p, Rows<D, MT>& R, int row_first, int rows, int pos0) {
-  const int g = (threadIdx.x & 31) >> 2;
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = row_first + 16 * t + g + 8 * r;
-      R.pos[t][r] = row < rows ? pos0 + row / p.G : -1;
-    }
   R.pos_min = row_first < rows ? pos0 + row_first / p.G : 0;
-  R.pos_max = row_first < rows ? pos0 + (min(rows, row_first + 16 * MT) - 1) / p.G : -1;
+  R.pos_max = row_first < rows ? pos0 + (min(rows, row_first + 8 * NT) - 1) / p.G : -1;
+  if constexpr (Queries<D, NT>::kRegs) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) Q.reg[n][s] = frag[n][s];
+  } else {
+    Q.mem = mem;
+    if (write) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; n += 2)
+          mem[(s * (NT / 2) + n / 2) * 32 + lane] = make_uint4(frag[n][s].x, frag[n][s].y, frag[n + 1][s].x, frag[n + 1][s].y);
+    }
+  }
 }
 
-// One stage of 32 tokens for the warp's rows.
-template <int D, bool INT8, int MT>
-__device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t* stage, const uint4* qf,
-                                         Rows<D, MT>& R, int base, int end) {
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// One stage of 32 tokens for the warp's rows.  FINE: weights as two f16 parts (22 bits), for an fp16 output,
+// beside whose own rounding one of 2^-12 a weight would show.
+template <int D, bool INT8, int NT, bool FINE>
+__device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t* stage, const Queries<D, NT>& Q,
+                                         Rows<D, NT>& R, int base) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float4 sc = *reinterpret_cast<const float4*>(stage + kStageTokens * D * 2);
   const int2 live = *reinterpret_cast<const int2*>(stage + kStageTokens * D * 2 + 16);
-  float s[MT][4][4];
+  float s[2][NT][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
-  // S = Q C_k^T: token tile j, lane (g, t) holds token 8 j + g, columns t and t + 4 of 16 codes
+      for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+  // S^T = C_k Q^T: 16-token tile i, the lane's tokens g and g + 8, columns t and t + 4 of 16 codes
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = 8 * j + g;
-    const uint8_t* src = stage + row * D;
+  for (int hh = 0; hh < D / 64; ++hh) {
+    uint4 c[4];
 #pragma unroll
-    for (int hh = 0; hh < D / 64; ++hh) {
-      const uint4 c = *reinterpret_cast<const uint4*>(src + swz<D>(row, t + 4 * hh) * 16);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    for (int x = 0; x < 4; ++x) {
+      const int row = 8 * x + g;
+      c[x] = *reinterpret_cast<const uint4*>(stage + row * D + swz<D>(row, t + 4 * hh) * 16);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t b0, b1;
-        codes_f16<INT8>(w[k], b0, b1);
+    for (int k = 0; k < 4; ++k) {
+      uint2 q[NT];
+      Q.get(hh * 4 + k, q);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint4 q = qf[(i * (D / 16) + hh * 4 + k) * 32 + lane];
-          const uint32_t a[4] = {q.x, q.y, q.z, q.w};
-          mma_f16(s[i][j], a, b0, b1);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const uint4 u = c[2 * i], w = c[2 * i + 1];
+        uint32_t a[4];
+        codes_f16<INT8>(k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w, a[0], a[2]);
+        codes_f16<INT8>(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w, a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(s[i][n], a, q[n].x, q[n].y);
       }
     }
   }
-  // A stage that every row sees whole needs no mask.
+  // Logits, and whether one passes its row's running maximum.  A stage that every row sees whole needs no mask.
   const bool whole = live.x == 16 && live.y == 16 && base + kStageTokens <= R.pos_min + 1 &&
                      (p.W == 0 || base > R.pos_max - p.W || base + kStageTokens <= p.S);
-  const uint32_t ref = max(R.ref, max(pow2_above(sc.z), pow2_above(sc.w)));
-  const float down = pow2_of(R.ref) * pow2_of(254u - ref);
-  const float v0 = sc.z * pow2_of(254u - ref), v1 = sc.w * pow2_of(254u - ref);
-  bool moved = ref != R.ref;
-  R.ref = ref;
-  float corr[MT][2];
+  float top[NT][2];
+  bool moved = false;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float f0 = sc.x * R.rf[i][r], f1 = sc.y * R.rf[i][r];
-      float top = -INFINITY;
+    for (int c = 0; c < 2; ++c) {
+      top[n][c] = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < 2; ++i) {
+        const float f = (i ? sc.y : sc.x) * R.rf[n][c];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float z = s[i][j][2 * r + e] * (j < 2 ? f0 : f1);
+          float z = s[i][n][2 * e + c] * f;
           if (!whole) {
-            const int in = 8 * (j & 1) + 2 * t + e;  // place within the group of 16
-            const int tok = base + 16 * (j >> 1) + in;
-            const bool seen = in < (j < 2 ? live.x : live.y) && tok <= R.pos[i][r] &&
-                              (p.W == 0 || tok > R.pos[i][r] - p.W || tok < p.S);
+            const int in = g + 8 * e, tok = base + 16 * i + in, pos = R.pos[n][c];
+            const bool seen = in < (i ? live.y : live.x) && tok <= pos && (p.W == 0 || tok > pos - p.W || tok < p.S);
             z = seen ? z : -INFINITY;
           }
-          s[i][j][2 * r + e] = z;
-          top = fmaxf(top, z);
+          s[i][n][2 * e + c] = z;
+          top[n][c] = fmaxf(top[n][c], z);
         }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float m = fmaxf(R.m[i][r], top);
-      const float shift = m == -INFINITY ? 0.f : m - 15.f;  // no token seen yet: every weight is 2^-inf
-      corr[i][r] = exp2_fast(R.m[i][r] - (m == -INFINITY ? 0.f : m));
-      moved |= m != R.m[i][r];
-      R.m[i][r] = m;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float w = exp2_fast(s[i][j][2 * r + e] - shift);
-          sum += w;
-          s[i][j][2 * r + e] = w * (j < 2 ? v0 : v1);
-        }
-      R.l[i][r] = R.l[i][r] * corr[i][r] + sum;
+      }
+      moved |= top[n][c] > R.m[n][c];
     }
-  if (__any_sync(0xffffffffu, moved)) {
+  const uint32_t ref = max(R.ref, max(pow2_above(sc.z), pow2_above(sc.w)));
+  if (__any_sync(0xffffffffu, moved || ref != R.ref)) {
+    const float down = pow2_of(R.ref) * pow2_of(254u - ref);
+    R.ref = ref;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const float c0 = corr[i][0] * down, c1 = corr[i][1] * down;
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        R.o[i][j][0] *= c0;
-        R.o[i][j][1] *= c0;
-        R.o[i][j][2] *= c1;
-        R.o[i][j][3] *= c1;
+      for (int c = 0; c < 2; ++c) {
+        float m = top[n][c];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        m = fmaxf(R.m[n][c], m);
+        f[c] = m == R.m[n][c] ? 1.f : exp2_fast(R.m[n][c] - m);  // 0 where no token was seen before
+        R.m[n][c] = m;
+        R.l[n][c] *= f[c];
+        f[c] *= down;
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        R.o[n][j][0] *= f[0];
+        R.o[n][j][1] *= f[1];
+        R.o[n][j][2] *= f[0];
+        R.o[n][j][3] *= f[1];
       }
     }
   }
-  // O += P C_v: 16 tokens at a time; the lane holds channels g D/8 .. of tokens 2t, 2t + 1, 2t + 8, 2t + 9, and
-  // product j covers channel j of every lane group
+  // Weights, rounded and transposed: b[i][n] are tokens 2 t, 2 t + 1 (and 8 more) of tile i for row g
+  const float v0 = sc.z * pow2_of(254u - ref), v1 = sc.w * pow2_of(254u - ref);
+  uint32_t b[2][NT][2], fine[FINE ? 2 : 1][FINE ? NT : 1][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // a row that has seen nothing: every logit is -inf, every weight 2^-inf
+    const float m0 = R.m[n][0] == -INFINITY ? 0.f : R.m[n][0] - 15.f, m1 = R.m[n][1] == -INFINITY ? 0.f : R.m[n][1] - 15.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float v = i ? v1 : v0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float w0 = exp2_fast(s[i][n][2 * e] - m0), w1 = exp2_fast(s[i][n][2 * e + 1] - m1);
+        R.l[n][0] += w0;
+        R.l[n][1] += w1;
+        const float u0 = w0 * v, u1 = w1 * v;
+        const uint32_t r = pack_half(u0, u1);
+        b[i][n][e] = transpose8(r);
+        if (FINE) {
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&r));
+          fine[FINE ? i : 0][FINE ? n : 0][e] = transpose8(pack_half(u0 - back.x, u1 - back.y));
+        }
+      }
+    }
+  }
+  // O^T += C_v^T P^T: the lane holds channels (D / 8) g .. of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of tile i
   const uint8_t* vst = stage + kStageTokens * D;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t a[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      a[i][0] = pack_half(s[i][2 * u][0], s[i][2 * u][1]);
-      a[i][1] = pack_half(s[i][2 * u][2], s[i][2 * u][3]);
-      a[i][2] = pack_half(s[i][2 * u + 1][0], s[i][2 * u + 1][1]);
-      a[i][3] = pack_half(s[i][2 * u + 1][2], s[i][2 * u + 1][3]);
-    }
+  for (int i = 0; i < 2; ++i) {
     uint32_t c[4][D / 32];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int row = 16 * u + 2 * t + (x & 1) + 8 * (x >> 1);
+      const int row = 16 * i + 2 * t + (x & 1) + 8 * (x >> 1);
       if (D == 128) {
         const uint4 w = *reinterpret_cast<const uint4*>(vst + row * D + swz<D>(row, g) * 16);
         c[x][0] = w.x, c[x][1] = w.y, c[x][D / 32 - 2] = w.z, c[x][D / 32 - 1] = w.w;
@@ -695,85 +744,123 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint32_t sel = hf ? 0x7362 : 0x5140;
-        uint32_t b0[2], b1[2];
-        codes_f16<INT8>(__byte_perm(c[0][w], c[1][w], sel), b0[0], b0[1]);
-        codes_f16<INT8>(__byte_perm(c[2][w], c[3][w], sel), b1[0], b1[1]);
+        uint32_t a[4];
+        codes_f16<INT8>(__byte_perm(c[0][w], c[1][w], sel), a[0], a[1]);
+        codes_f16<INT8>(__byte_perm(c[2][w], c[3][w], sel), a[2], a[3]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) mma_f16(R.o[i][w * 4 + hf * 2 + x], a[i], b0[x], b1[x]);
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(R.o[n][2 * w + hf], a, b[i][n][0], b[i][n][1]);
+          if (FINE) mma_f16(R.o[n][2 * w + hf], a, fine[FINE ? i : 0][FINE ? n : 0][0], fine[FINE ? i : 0][FINE ? n : 0][1]);
+        }
       }
   }
 }
 
-// Completes a row's sums over the four lanes that share it.
-template <int D, int MT>
-__device__ __forceinline__ void finish_sums(Rows<D, MT>& R) {
+// Completes the rows' sums over the 8 lanes that share them.
+template <int D, int NT>
+__device__ __forceinline__ void finish_sums(Rows<D, NT>& R) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float l = R.l[i][r];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      R.l[i][r] = l;
+    for (int c = 0; c < 2; ++c) {
+      float l = R.l[n][c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      R.l[n][c] = l;
     }
+}
+// Writes column c of tile n, scaled, as the lane's D / 8 channels of a row.
+template <int D, int NT>
+__device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, float f, float* row) {
+  float* o = row + ((threadIdx.x & 31) >> 2) * (D / 8);
+#pragma unroll
+  for (int j = 0; j < D / 16; j += 2)
+    *reinterpret_cast<float4*>(o + 2 * j) = make_float4(R.o[n][j][c] * f, R.o[n][j][2 + c] * f, R.o[n][j + 1][c] * f, R.o[n][j + 1][2 + c] * f);
 }
 
 // ---- the narrow form: up to 32 rows a KV head -----------------------------------------------------
 //
 // Bound by the codes' bytes.  The stages of all (sequence, KV head) units form one
-// line that n_cta CTAs cut into equal parts, so ragged batches keep every SM busy
+// line that the CTAs cut into equal parts, so ragged batches keep every SM busy
 // to the end; the four warps of a CTA take its stages in turn, each through a ring
 // of its own (no barrier in the loop), and are joined at each unit's end.  A unit
 // that more than one CTA worked on is joined by paged_join_kernel.
 
 __device__ __forceinline__ Span seq_span(const PagedAttnParams& p, const Seq& s) {
-  const int pos0 = s.len - s.n;
   if (s.n == 0) return Span{0, 0, 0, 0, 0};
-  return make_span(max(pos0, 0), s.len - 1, p.W, p.S);
+  return make_span(max(s.len - s.n, 0), s.len - 1, p.W, p.S);
 }
 
-// Stages of a sequence (for one KV head).
-__device__ __forceinline__ int seq_stages(const PagedAttnParams& p, int b) {
+// The line's geometry, in all lanes of a warp.  Stage counts fit 31 bits (the host
+// refuses more).
+struct Line {
+  uint32_t total;   // stages in all
+  uint32_t per;     // of each CTA: a multiple of its warps
+  uint32_t mine;    // lane's: stages of all units of sequence `lane`, and those before it
+  uint32_t before;
+};
+
+// Stages of all of a sequence's units.
+__device__ __forceinline__ uint32_t seq_stages(const PagedAttnParams& p, int b) {
   bool bad;
   const Seq s = read_seq(p.b, b, p.c.P, &bad);
-  return seq_span(p, s).stages;
+  return (uint32_t)seq_span(p, s).stages * (uint32_t)p.c.Hkv;
 }
-// All lanes: the stages of all units.
-__device__ __forceinline__ int64_t line_total(const PagedAttnParams& p) {
-  const int lane = threadIdx.x & 31;
-  int64_t sum = 0;
-  for (int b = lane; b < p.b.B; b += 32) sum += seq_stages(p, b);
+__device__ __forceinline__ uint32_t warp_sum(uint32_t x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.c.Hkv;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
-// All lanes: the sequence that stage x of the line lies in, and the line's stage
-// at which its first unit begins.
-__device__ __forceinline__ int line_find(const PagedAttnParams& p, int64_t x, int64_t& begin) {
+__device__ __forceinline__ uint32_t warp_upto(uint32_t x) {  // inclusive prefix sum over the lanes
   const int lane = threadIdx.x & 31;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < p.b.B; b0 += 32) {
-    int64_t mine = b0 + lane < p.b.B ? (int64_t)seq_stages(p, b0 + lane) * p.c.Hkv : 0;
-    int64_t upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > x);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ Line make_line(const PagedAttnParams& p) {
+  const int lane = threadIdx.x & 31;
+  Line l;
+  l.mine = lane < p.b.B ? seq_stages(p, lane) : 0;
+  const uint32_t upto = warp_upto(l.mine);
+  l.before = upto - l.mine;
+  l.total = __shfl_sync(0xffffffffu, upto, 31);
+  if (p.b.B > 32) {
+    uint32_t sum = 0;
+    for (int b = 32 + lane; b < p.b.B; b += 32) sum += seq_stages(p, b);
+    l.total += warp_sum(sum);
+  }
+  const uint32_t n = (uint32_t)p.n_cta * kWarps;
+  l.per = ((l.total + n - 1) / n) * kWarps;
+  return l;
+}
+// The sequence that stage x < total lies in, and the stage at which its first unit begins.
+__device__ __forceinline__ int line_find(const PagedAttnParams& p, const Line& l, uint32_t x, uint32_t& begin) {
+  const int lane = threadIdx.x & 31;
+  uint32_t past = __ballot_sync(0xffffffffu, l.before + l.mine > x);
+  if (past) {
+    const int at = __ffs(past) - 1;
+    begin = __shfl_sync(0xffffffffu, l.before, at);
+    return at;
+  }
+  uint32_t before = __shfl_sync(0xffffffffu, l.before + l.mine, 31);
+  for (int b0 = 32; b0 < p.b.B; b0 += 32) {
+    const uint32_t mine = b0 + lane < p.b.B ? seq_stages(p, b0 + lane) : 0;
+    const uint32_t upto = before + warp_upto(mine);
+    past = __ballot_sync(0xffffffffu, upto > x);
     if (past) {
-      const int l = __ffs(past) - 1;
-      begin = __shfl_sync(0xffffffffu, before + upto - mine, l);
-      return b0 + l;
+      const int at = __ffs(past) - 1;
+      begin = __shfl_sync(0xffffffffu, upto - mine, at);
+      return b0 + at;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before = __shfl_sync(0xffffffffu, upto, 31);
   }
   begin = before;
-  return p.b.B;
+  return p.b.B - 1;
 }
-__device__ __forceinline__ int64_t cut(int64_t total, int n, int c) { return total * c / n; }
 
 __device__ __forceinline__ void store_row(const PagedAttnParams& p, int64_t tok, int head, float lse2) {
   if (p.lse != nullptr) p.lse[tok * p.Hq + head] = lse2;
@@ -783,33 +870,42 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Natural logarithm of the sum whose weights are 2^(z - m + 15).
 __device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m - 15.f + log2f(l)) * kLn2; }
 
-template <int D, bool INT8, int MT>
-__global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, MT>::kCtas) paged_narrow_kernel(const PagedAttnParams p) {
+__device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t tok, int hd, int D, int c, const float4& y,
+                                             float m, float l) {
+  *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + 4 * c) =
+      make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
+  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+}
+
+template <int D, bool INT8, int NT, bool FINE>
+__global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, NT>::kCtas) paged_narrow_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kRing = NarrowGeo<D, MT>::kStages, kBytes = StageGeo<D>::kBytes;
+  constexpr int kRing = NarrowGeo<D, NT>::kStages, kBytes = StageGeo<D>::kBytes, kRows = 8 * NT;
+  // a joined row's place: D floats and 4 more, so that rows begin in different banks
+  constexpr int kRowFloats = D + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kRing * kBytes;
-  uint4* qf = reinterpret_cast<uint4*>(smem + kWarps * kRing * kBytes);
+  uint4* qmem = reinterpret_cast<uint4*>(smem + kWarps * kRing * kBytes);
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
 
-  const int64_t total = line_total(p);
-  const int64_t first = cut(total, p.n_cta, blockIdx.x), last = cut(total, p.n_cta, blockIdx.x + 1);
-  int64_t at = first;
+  const Line line = make_line(p);
+  const uint32_t first = min(line.per * blockIdx.x, line.total), last = min(first + line.per, line.total);
+  uint32_t at = first;
   pdl_allow_dependents();  // the join may take its place; it waits for this grid's end
   while (at < last) {
     // the unit that stage `at` lies in, and the part of it that is this CTA's
-    int64_t begin;
-    const int b = line_find(p, at, begin);
+    uint32_t begin;
+    const int b = line_find(p, line, at, begin);
     bool bad;
     const Seq seq = read_seq(p.b, b, p.c.P, &bad);
     const Span span = seq_span(p, seq);
-    const int h = (int)((at - begin) / span.stages);
-    const int64_t ubegin = begin + (int64_t)h * span.stages;
-    const int s0 = (int)(at - ubegin), s1 = (int)min((int64_t)span.stages, last - ubegin);
+    const int h = (int)((at - begin) / (uint32_t)span.stages);
+    const uint32_t ubegin = begin + (uint32_t)h * span.stages;
+    const int s0 = (int)(at - ubegin), s1 = (int)min((uint32_t)span.stages, last - ubegin);
     const bool complete = s0 == 0 && s1 == span.stages;
     const int slot = 2 * blockIdx.x + (at == first ? 0 : 1);
     at = ubegin + s1;
-    const int rows = min(seq.n * p.G, 16 * MT), pos0 = seq.len - seq.n;
+    const int rows = min(seq.n * p.G, kRows), pos0 = seq.len - seq.n;
     const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
     if (bad && h == 0 && s0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
 
@@ -830,12 +926,11 @@ __global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, MT>::kCtas) paged_na
       }
       cp_commit();
     }
-    Rows<D, MT> R;
+    Rows<D, NT> R;
+    Queries<D, NT> Q;
     R.clear();
-    set_rows<D, MT>(p, R, 0, rows, pos0);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) load_q_tile<D>(p, qf + i * (D / 16) * 32, seq.t0, h, 16 * i, rows, R.rf[i], warp == i);
-    __syncthreads();
+    load_rows<D, NT>(p, Q, R, qmem, seq.t0, h, 0, rows, pos0, warp == 0);
+    if (!Queries<D, NT>::kRegs) __syncthreads();
 
     int slot_in = kRing - 1, slot_out = 0;
     for (int i = 0; i < mine; ++i) {
@@ -848,66 +943,52 @@ __global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, MT>::kCtas) paged_na
       cp_commit();
       int sb, se;
       stage_range(span, s0 + warp + i * kWarps, sb, se);
-      do_stage<D, INT8, MT>(p, ring + slot_out * kBytes, qf, R, sb, se);
+      do_stage<D, INT8, NT, FINE>(p, ring + slot_out * kBytes, Q, R, sb);
       __syncwarp();
       slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
       slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
     }
     cp_wait<0>();
-    finish_sums<D, MT>(R);
+    finish_sums<D, NT>(R);
 
-    // Join the warps: sums and maxima first, then the outputs, through the rings' memory.
+    // Join the warps through the rings' memory: [warp][row][D outputs, m, l, ref].
     __syncthreads();
-    float* head = reinterpret_cast<float*>(qf);  // [warp][row][m, l, ref]
-    float* body = reinterpret_cast<float*>(smem);  // [warp][row][D]
+    float* body = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * i + g + 8 * r;
-        if (t == 0) {
-          float* e = head + (warp * 16 * MT + row) * 3;
-          e[0] = R.m[i][r], e[1] = R.l[i][r], e[2] = pow2_of(R.ref);
-        }
-        // lane (g, t) holds channels 2 t and 2 t + 1 of the 8 lane groups: product j's columns are channel j of group 2 t
-        float* o = body + (warp * 16 * MT + row) * D;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[(2 * t) * (D / 8) + j] = R.o[i][j][2 * r];
-          o[(2 * t + 1) * (D / 8) + j] = R.o[i][j][2 * r + 1];
-        }
+      for (int c = 0; c < 2; ++c) {
+        float* e = body + (warp * kRows + 8 * n + 2 * t + c) * kRowFloats;
+        put_row<D, NT>(R, n, c, 1.f, e);
+        if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c], e[D + 2] = pow2_of(R.ref);
       }
     __syncthreads();
     for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
       const int row = x / (D / 4), c = x % (D / 4) * 4;
+      const float* e = body + row * kRowFloats;
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, head[(w * 16 * MT + row) * 3]);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, e[w * kRows * kRowFloats + D]);
       float l = 0.f, f[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float* e = head + (w * 16 * MT + row) * 3;
-        f[w] = m == -INFINITY ? 0.f : exp2f(e[0] - m);
-        l += e[1] * f[w];
+        f[w] = m == -INFINITY ? 0.f : exp2_fast(e[w * kRows * kRowFloats + D] - m);
+        l += e[w * kRows * kRowFloats + D + 1] * f[w];
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(body + (w * 16 * MT + row) * D + c);
-        const float k = f[w] * inv * head[(w * 16 * MT + row) * 3 + 2];
+        const float4 o = *reinterpret_cast<const float4*>(e + w * kRows * kRowFloats + c);
+        const float k = f[w] * inv * e[w * kRows * kRowFloats + D + 2];
         y.x += o.x * k, y.y += o.y * k, y.z += o.z * k, y.w += o.w * k;
       }
-      const int64_t tok = seq.t0 + row / p.G;
-      const int hd = h * p.G + row % p.G;
       if (complete) {
-        *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + c) =
-            make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
-        if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+        store_joined(p, seq.t0 + row / p.G, h * p.G + row % p.G, D, c / 4, y, m, l);
       } else {
-        float* ws = p.ws + ((int64_t)slot * 16 * MT + row) * (D + 4);
+        float* ws = p.ws + ((int64_t)slot * kRows + row) * (D + 4);
         *reinterpret_cast<float4*>(ws + c) = y;
-        if (c == 0) ws[D] = m, ws[D + 1] = l;
+        if (c == 0) *reinterpret_cast<float2*>(ws + D) = make_float2(m, l);
       }
     }
     __syncthreads();
@@ -924,8 +1005,14 @@ __device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& s
   __shared__ float weight[kJoinMost], red[2][kJoinThreads / 32];
   __shared__ float4 acc[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31;
+  float2 e[kJoinMost / kJoinThreads];
   float m = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, part(i)[D]);
+#pragma unroll
+  for (int k = 0; k < kJoinMost / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    e[k] = i < n ? *reinterpret_cast<const float2*>(part(i) + D) : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, e[k].x);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[0][tid >> 5] = m;
@@ -933,10 +1020,11 @@ __device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& s
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
   float l = 0.f;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float* e = part(i);
-    const float w = m == -INFINITY ? 0.f : exp2f(e[D] - m) * e[D + 1];
-    weight[i] = w;
+#pragma unroll
+  for (int k = 0; k < kJoinMost / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    const float w = m == -INFINITY ? 0.f : exp2_fast(e[k].x - m) * e[k].y;
+    if (i < n) weight[i] = w;
     l += w;
   }
 #pragma unroll
@@ -971,13 +1059,6 @@ __device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& s
   return y;
 }
 
-__device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t tok, int hd, int D, int c, const float4& y,
-                                             float m, float l) {
-  *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + 4 * c) =
-      make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
-  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
-}
-
 // Joins the parts of units that more than one CTA worked on, and writes the rows
 // of units with no visible token.  One CTA a (unit, row).
 template <int D>
@@ -999,34 +1080,22 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
     return;
   }
   // the line up to this sequence
-  const int lane = threadIdx.x & 31;
-  int64_t before = 0, total = 0;
-  for (int i = lane; i < p.b.B; i += 32) {
-    const int64_t n = seq_stages(p, i);
-    total += n;
-    before += i < b ? n : 0;
+  const Line line = make_line(p);
+  uint32_t begin = __shfl_sync(0xffffffffu, line.before, b & 31);
+  if (b >= 32) {
+    uint32_t sum = 0;
+    for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_stages(p, i);
+    begin = warp_sum(sum);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  total *= p.c.Hkv;
-  const int64_t begin = before * p.c.Hkv + (int64_t)h * stages, endu = begin + stages;
-  // the CTA whose part [total c / n, total (c + 1) / n) holds a stage x is c = ceil((x + 1) n / total) - 1;
-  // with fewer stages than CTAs the parts are of one stage or none, and those in between that have none are passed over
-  const int c0 = (int)(((begin + 1) * p.n_cta + total - 1) / total) - 1;
-  const int c1 = (int)((endu * p.n_cta + total - 1) / total) - 1;
+  begin += (uint32_t)h * stages;
+  const uint32_t c0 = begin / line.per, c1 = (begin + stages - 1) / line.per;
   pdl_wait_primary();
   if (c0 == c1) return;  // complete in one CTA
-  const bool sparse = total < p.n_cta;
-  const int n = sparse ? stages : c1 - c0 + 1;
-  const bool starts_before = cut(total, p.n_cta, c0) < begin;
+  const uint32_t late = c0 * line.per < begin ? 1 : 0;  // the first part is not its CTA's first
   auto part = [&](int i) -> const float* {
-    const int c = sparse ? (int)(((begin + i + 1) * p.n_cta + total - 1) / total) - 1 : c0 + i;
-    const int64_t slot = 2 * (int64_t)c + (i == 0 && starts_before ? 1 : 0);
-    return p.ws + (slot * tile_rows + row) * (D + 4);
+    return p.ws + ((int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * tile_rows + row) * (D + 4);
   };
+  const int n = (int)(c1 - c0) + 1;
   float m, l;
   const float4 y = join_parts<D>(n, part, m, l);
   if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, y, m, l);
@@ -1041,12 +1110,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
 
 constexpr int kWideRing = 4;
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool FINE>
 __global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int MT = 2, kBytes = StageGeo<D>::kBytes;
+  constexpr int NT = 4, kBytes = StageGeo<D>::kBytes, kRowFloats = D + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint4* qf = reinterpret_cast<uint4*>(smem + kWideRing * kBytes);
+  uint4* qmem = reinterpret_cast<uint4*>(smem + kWideRing * kBytes) + warp * (NT / 2) * (D / 16) * 32;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
   const int unit = blockIdx.y, b = unit / p.c.Hkv, h = unit % p.c.Hkv;
   // the tiles that see most come first
@@ -1078,12 +1147,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel
     }
     cp_commit();
   }
-  Rows<D, MT> R;
+  Rows<D, NT> R;
+  Queries<D, NT> Q;
   R.clear();
-  set_rows<D, MT>(p, R, row0 + 32 * warp, rows, pos0);
-  uint4* my = qf + warp * MT * (D / 16) * 32;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) load_q_tile<D>(p, my + i * (D / 16) * 32, seq.t0, h, row0 + 32 * warp + 16 * i, rows, R.rf[i], true);
+  load_rows<D, NT>(p, Q, R, qmem, seq.t0, h, row0 + 32 * warp, rows, pos0, true);
   for (int i = s0; i < s1; ++i) {
     cp_wait<kWideRing - 2>();
     __syncthreads();  // the stage is there, and everyone is done with the one before
@@ -1095,43 +1162,36 @@ __global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel
     cp_commit();
     int sb, se;
     stage_range(span, i, sb, se);
-    if (sb <= R.pos_max) do_stage<D, INT8, MT>(p, smem + (i - s0) % kWideRing * kBytes, my, R, sb, se);
+    if (sb <= R.pos_max) do_stage<D, INT8, NT, FINE>(p, smem + (i - s0) % kWideRing * kBytes, Q, R, sb);
   }
   cp_wait<0>();
-  finish_sums<D, MT>(R);
-  // Rows leave through shared memory, a warp's 16 at a time, so that they are stored in their own order.
+  finish_sums<D, NT>(R);
+  // Rows leave through shared memory, 8 of a warp's at a time, so that they are stored in their own order.
   __syncthreads();
-  float* body = reinterpret_cast<float*>(smem) + warp * 16 * (D + 4);
+  float* body = reinterpret_cast<float*>(smem) + warp * 8 * kRowFloats;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
+  for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float inv = R.l[i][r] == 0.f ? 0.f : pow2_of(R.ref) / R.l[i][r];
-      float* o = body + (g + 8 * r) * (D + 4);
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        o[(2 * t) * (D / 8) + j] = R.o[i][j][2 * r] * inv;
-        o[(2 * t + 1) * (D / 8) + j] = R.o[i][j][2 * r + 1] * inv;
-      }
-      if (t == 0) o[D] = R.m[i][r], o[D + 1] = R.l[i][r];
+    for (int c = 0; c < 2; ++c) {
+      float* e = body + (2 * t + c) * kRowFloats;
+      put_row<D, NT>(R, n, c, R.l[n][c] == 0.f ? 0.f : pow2_of(R.ref) / R.l[n][c], e);
+      if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c];
     }
     __syncwarp();
-    const int first = row0 + 32 * warp + 16 * i;
-    for (int x = lane; x < 16 * (D / 4); x += 32) {
+    const int first = row0 + 32 * warp + 8 * n;
+    for (int x = lane; x < 8 * (D / 4); x += 32) {
       const int rr = x / (D / 4), c = x % (D / 4) * 4, row = first + rr;
       if (row >= rows) break;
-      const float4 y = *reinterpret_cast<const float4*>(body + rr * (D + 4) + c);
-      const float m = body[rr * (D + 4) + D], l = body[rr * (D + 4) + D + 1];
+      const float* e = body + rr * kRowFloats;
+      const float4 y = *reinterpret_cast<const float4*>(e + c);
       const int64_t tok = seq.t0 + row / p.G;
       const int hd = h * p.G + row % p.G;
       if (p.n_splits == 1) {
-        *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + c) =
-            make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
-        if (c == 0) store_row(p, tok, hd, lse_of(m, l));
+        store_joined(p, tok, hd, D, c / 4, y, e[D], e[D + 1]);
       } else {
         float* ws = p.ws + (((int64_t)split * p.b.n_new + tok) * p.Hq + hd) * (D + 4);
         *reinterpret_cast<float4*>(ws + c) = y;
-        if (c == 0) ws[D] = m, ws[D + 1] = l;
+        if (c == 0) *reinterpret_cast<float2*>(ws + D) = make_float2(e[D], e[D + 1]);
       }
     }
     __syncwarp();
@@ -1172,26 +1232,32 @@ cudaError_t launch(void (*f)(A...), dim3 grid, dim3 block, size_t smem, bool cha
   return cudaLaunchKernelEx(&c, f, args...);
 }
 
-template <int D, bool INT8, int MT>
+template <int D, bool INT8, int NT, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
-  constexpr size_t rings = (size_t)kWarps * NarrowGeo<D, MT>::kStages * StageGeo<D>::kBytes;
-  constexpr size_t frags = (size_t)MT * (D / 16) * 32 * sizeof(uint4);
-  static_assert(rings >= (size_t)kWarps * 16 * MT * D * sizeof(float), "the join's rows fit the rings");
-  static_assert(frags >= (size_t)kWarps * 16 * MT * 3 * sizeof(float), "the join's sums fit the fragments");
-  cudaError_t e = launch(paged_narrow_kernel<D, INT8, MT>, dim3(p.n_cta), dim3(kWarps * 32), rings + frags, false, s, p);
+  constexpr size_t rings = (size_t)kWarps * NarrowGeo<D, NT>::kStages * StageGeo<D>::kBytes;
+  constexpr size_t frags = Queries<D, NT>::kRegs ? 0 : (size_t)(NT / 2) * (D / 16) * 32 * sizeof(uint4);
+  constexpr size_t rows = (size_t)kWarps * 8 * NT * (D + 4) * sizeof(float);
+  constexpr size_t smem = rings + frags > rows ? rings + frags : rows;
+  cudaError_t e = launch(paged_narrow_kernel<D, INT8, NT, FINE>, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess) return e;
-  const int rows = p.b.max_new * p.G < 16 * MT ? p.b.max_new * p.G : 16 * MT;
-  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, rows), dim3(kJoinThreads), 0, true, s, p, 16 * MT);
+  const int n = p.b.max_new * p.G < 8 * NT ? p.b.max_new * p.G : 8 * NT;
+  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, 8 * NT);
+}
+template <int D, bool INT8>
+cudaError_t narrow(const PagedAttnParams& p, int tiles, cudaStream_t s) {
+  if (p.half)
+    return tiles == 1 ? narrow<D, INT8, 1, true>(p, s) : tiles == 2 ? narrow<D, INT8, 2, true>(p, s) : narrow<D, INT8, 4, true>(p, s);
+  return tiles == 1 ? narrow<D, INT8, 1, false>(p, s) : tiles == 2 ? narrow<D, INT8, 2, false>(p, s) : narrow<D, INT8, 4, false>(p, s);
 }
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool FINE>
 cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   constexpr size_t ring = (size_t)kWideRing * StageGeo<D>::kBytes;
   constexpr size_t frags = (size_t)kWarps * 2 * (D / 16) * 32 * sizeof(uint4);
-  constexpr size_t out = (size_t)kWarps * 16 * (D + 4) * sizeof(float);
-  constexpr size_t smem = ring + frags > out ? ring + frags : out;
+  constexpr size_t smem = ring + frags;
+  static_assert(smem >= (size_t)kWarps * 8 * (D + 4) * sizeof(float), "the rows that leave fit");
   const int64_t tiles = ((int64_t)p.b.max_new * p.G + kWideRows - 1) / kWideRows;
-  cudaError_t e = launch(paged_wide_kernel<D, INT8>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
+  cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
                          dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(kJoinThreads), 0, true, s, p);
@@ -1209,16 +1275,17 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int tiles, cudaStream_t s) {
-  if (D == 128)
-    return int8 ? (tiles == 1 ? narrow<128, true, 1>(p, s) : narrow<128, true, 2>(p, s))
-                : (tiles == 1 ? narrow<128, false, 1>(p, s) : narrow<128, false, 2>(p, s));
-  return int8 ? (tiles == 1 ? narrow<64, true, 1>(p, s) : narrow<64, true, 2>(p, s))
-              : (tiles == 1 ? narrow<64, false, 1>(p, s) : narrow<64, false, 2>(p, s));
+  if (D == 128) return int8 ? narrow<128, true>(p, tiles, s) : narrow<128, false>(p, tiles, s);
+  return int8 ? narrow<64, true>(p, tiles, s) : narrow<64, false>(p, tiles, s);
 }
 
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s) {
-  if (D == 128) return int8 ? wide<128, true>(p, s) : wide<128, false>(p, s);
-  return int8 ? wide<64, true>(p, s) : wide<64, false>(p, s);
+  if (p.half) {
+    if (D == 128) return int8 ? wide<128, true, true>(p, s) : wide<128, false, true>(p, s);
+    return int8 ? wide<64, true, true>(p, s) : wide<64, false, true>(p, s);
+  }
+  if (D == 128) return int8 ? wide<128, true, false>(p, s) : wide<128, false, false>(p, s);
+  return int8 ? wide<64, true, false>(p, s) : wide<64, false, false>(p, s);
 }
 
 }  // namespace hyb

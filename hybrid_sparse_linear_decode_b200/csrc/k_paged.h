@@ -56,11 +56,11 @@ struct PagedAttnParams {
 };
 
 // Rows (new tokens x heads of a group) of one sequence and KV head that the
-// narrow form takes: two 16-row matrix tiles.
+// narrow form takes: 1, 2 or 4 matrix tiles of 8 rows.
 constexpr int kNarrowRows = 32;
 constexpr int kWideRows = 128;  // rows of a CTA of the wide form
 constexpr int kWideCtasPerSm = 2;
-constexpr int narrow_ctas_per_sm(int tiles) { return tiles == 1 ? 3 : 2; }
+constexpr int narrow_ctas_per_sm(int tiles) { return tiles <= 2 ? 3 : 2; }
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int tiles, cudaStream_t s);

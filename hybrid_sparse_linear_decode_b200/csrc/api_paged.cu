@@ -56,14 +56,13 @@ bool rows_ok(const void* p, int64_t stride, int64_t heads, int d, int64_t unit) 
 }
 
 struct Plan {
-  int tiles;     // 8-row tiles of the narrow form (1, 2 or 4); 0 selects the wide form
+  int rows;      // of the narrow form (8, 16, 32 or 64); 0 selects the wide form
   int n_cta;     // narrow
   int n_splits;  // wide
   size_t bytes;
 };
 
-// Narrow up to 32 rows a KV head: the row tiles share one conversion of the codes, and more than four do not fit
-// the registers.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
+// Narrow up to 64 rows a KV head, 16 a warp.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
 // Wide: as many parts of each row tile's stages as fill the SMs, each of at least 8 stages.
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink) {
   Plan p{};
@@ -75,12 +74,12 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   const int64_t stages = std::max<int64_t>(1, (len + 31) / 32);
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
   if (rows <= kNarrowRows) {
-    p.tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * narrow_ctas_per_sm(p.tiles), (units * stages + 3) / 4));
-    p.bytes = (size_t)2 * p.n_cta * 8 * p.tiles * row_bytes;
+    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * kCtasPerSm, (units * stages + 3) / 4));
+    p.bytes = (size_t)2 * p.n_cta * p.rows * row_bytes;
   } else {
     const int64_t tiles = units * ((rows + kWideRows - 1) / kWideRows);
-    int64_t n = tiles >= kSms * kWideCtasPerSm ? 1 : (kSms * kWideCtasPerSm + tiles - 1) / tiles;
+    int64_t n = tiles >= kSms * kCtasPerSm ? 1 : (kSms * kCtasPerSm + tiles - 1) / tiles;
     n = std::max<int64_t>(1, std::min<int64_t>({n, stages / 8, 64}));
     if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
     p.n_splits = (int)n;
@@ -180,7 +179,7 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   p.ws = static_cast<float*>(workspace);
   p.status = batch->status;
   const int int8 = cache->code == HYB_CODE_INT8;
-  const cudaError_t e = plan.tiles > 0 ? launch_paged_narrow(p, d, int8, plan.tiles, stream) : launch_paged_wide(p, d, int8, stream);
+  const cudaError_t e = plan.rows > 0 ? launch_paged_narrow(p, d, int8, plan.rows, stream) : launch_paged_wide(p, d, int8, stream);
   return e == cudaSuccess ? HYB_OK : record_cuda_error(e);
 }
 

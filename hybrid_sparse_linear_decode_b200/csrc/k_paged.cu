@@ -332,11 +332,11 @@ template <int D>
 struct StageGeo {
   static constexpr int kBytes = kStageTokens * D * 2 + 32;  // K codes, V codes, scales and flags
 };
-// Narrow form: CTAs an SM (registers: 168 or 255 a thread) and stages of each warp's ring.
-template <int D, int NT>
+// Narrow form: a team of GW warps shares the stages of a ring, each warp with 8 NT rows of its own.
+template <int D, int GW>
 struct NarrowGeo {
-  static constexpr int kCtas = narrow_ctas_per_sm(NT);
-  static constexpr int kStages = D == 128 ? (kCtas == 3 ? 2 : 3) : (kCtas == 3 ? 4 : 5);
+  static constexpr int kTeams = kWarps / GW;
+  static constexpr int kStages = (D == 128 ? 2 : 4) * GW;
 };
 
 // 16-byte column of a stage row, moved so that the reads of both products meet
@@ -510,36 +510,18 @@ struct Rows {
 };
 
 // Query fragments of NT row tiles: for k-step s, channels 16 t + 4 s .. + 3 (64 more for the upper half of D = 128)
-// of row g.  Up to 16 rows stay in registers, 32 rows go through shared memory (in pairs of tiles, [s][pair][lane]).
+// of row g.
 template <int D, int NT>
 struct Queries {
-  static constexpr bool kRegs = NT <= 2;
-  uint2 reg[kRegs ? NT : 1][kRegs ? D / 16 : 1];
-  const uint4* mem;
-
-  __device__ __forceinline__ void get(int s, uint2 (&q)[NT]) const {
-    if (kRegs) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) q[n] = reg[kRegs ? n : 0][kRegs ? s : 0];
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        const uint4 x = mem[(s * (NT / 2) + n / 2) * 32 + (threadIdx.x & 31)];
-        q[n] = make_uint2(x.x, x.y);
-        q[n + 1 < NT ? n + 1 : n] = make_uint2(x.z, x.w);
-      }
-    }
-  }
+  uint2 frag[NT][D / 16];
 };
 
-// Loads the fragments of rows row_first .. and the rows' factors and positions.  `mem` (32 rows only): where the
-// fragments go; of the warps that share it those with `write` store them.
+// Loads the fragments of rows row_first .., and the rows' factors and positions.
 template <int D, int NT>
-__device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, NT>& Q, Rows<D, NT>& R, uint4* mem,
-                                          int t0, int h, int row_first, int rows, int pos0, bool write) {
+__device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, NT>& Q, Rows<D, NT>& R, int t0, int h,
+                                          int row_first, int rows, int pos0) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool half = p.half != 0;
-  uint2 frag[NT][D / 16];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int row = row_first + 8 * n + g;
@@ -570,7 +552,7 @@ __device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, N
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const float* y = x[s >> 2] + 4 * (s & 3);
-      frag[n][s] = make_uint2(pack_half(y[0] * inv, y[1] * inv), pack_half(y[2] * inv, y[3] * inv));
+      Q.frag[n][s] = make_uint2(pack_half(y[0] * inv, y[1] * inv), pack_half(y[2] * inv, y[3] * inv));
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -581,21 +563,6 @@ __device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, N
   }
   R.pos_min = row_first < rows ? pos0 + row_first / p.G : 0;
   R.pos_max = row_first < rows ? pos0 + (min(rows, row_first + 8 * NT) - 1) / p.G : -1;
-  if constexpr (Queries<D, NT>::kRegs) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) Q.reg[n][s] = frag[n][s];
-  } else {
-    Q.mem = mem;
-    if (write) {
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int n = 0; n < NT; n += 2)
-          mem[(s * (NT / 2) + n / 2) * 32 + lane] = make_uint4(frag[n][s].x, frag[n][s].y, frag[n + 1][s].x, frag[n + 1][s].y);
-    }
-  }
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -630,8 +597,6 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint2 q[NT];
-      Q.get(hh * 4 + k, q);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint4 u = c[2 * i], w = c[2 * i + 1];
@@ -639,7 +604,7 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
         codes_f16<INT8>(k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w, a[0], a[2]);
         codes_f16<INT8>(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w, a[1], a[3]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(s[i][n], a, q[n].x, q[n].y);
+        for (int n = 0; n < NT; ++n) mma_f16(s[i][n], a, Q.frag[n][hh * 4 + k].x, Q.frag[n][hh * 4 + k].y);
       }
     }
   }
@@ -779,13 +744,13 @@ __device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, floa
     *reinterpret_cast<float4*>(o + 2 * j) = make_float4(R.o[n][j][c] * f, R.o[n][j][2 + c] * f, R.o[n][j + 1][c] * f, R.o[n][j + 1][2 + c] * f);
 }
 
-// ---- the narrow form: up to 32 rows a KV head -----------------------------------------------------
+// ---- the narrow form: up to 64 rows a KV head -----------------------------------------------------
 //
 // Bound by the codes' bytes.  The stages of all (sequence, KV head) units form one
 // line that the CTAs cut into equal parts, so ragged batches keep every SM busy
-// to the end; the four warps of a CTA take its stages in turn, each through a ring
-// of its own (no barrier in the loop), and are joined at each unit's end.  A unit
-// that more than one CTA worked on is joined by paged_join_kernel.
+// to the end; the teams of a CTA (one, two or four warps that share a ring, with 8 or
+// 16 rows each) take its stages in turn and are joined at each unit's end.  A unit that
+// more than one CTA worked on is joined by paged_join_kernel.
 
 __device__ __forceinline__ Span seq_span(const PagedAttnParams& p, const Seq& s) {
   if (s.n == 0) return Span{0, 0, 0, 0, 0};
@@ -877,15 +842,27 @@ __device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t t
   if (c == 0) store_row(p, tok, hd, lse_of(m, l));
 }
 
-template <int D, bool INT8, int NT, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, NT>::kCtas) paged_narrow_kernel(const PagedAttnParams p) {
+template <int GW>
+__device__ __forceinline__ void team_sync() {
+  if (GW == 1) {
+    __syncwarp();
+  } else if (GW == kWarps) {
+    __syncthreads();
+  } else {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)(threadIdx.x >> 5) / GW), "n"(GW * 32) : "memory");
+  }
+}
+
+template <int D, bool INT8, int NT, int GW, bool FINE>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kRing = NarrowGeo<D, NT>::kStages, kBytes = StageGeo<D>::kBytes, kRows = 8 * NT;
+  constexpr int kTeams = NarrowGeo<D, GW>::kTeams, kRing = NarrowGeo<D, GW>::kStages, kBytes = StageGeo<D>::kBytes;
+  constexpr int kRows = 8 * NT * GW;
   // a joined row's place: D floats and 4 more, so that rows begin in different banks
   constexpr int kRowFloats = D + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * kRing * kBytes;
-  uint4* qmem = reinterpret_cast<uint4*>(smem + kWarps * kRing * kBytes);
+  const int team = warp / GW, member = warp % GW, me = threadIdx.x % (GW * 32);
+  uint8_t* ring = smem + team * kRing * kBytes;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
 
   const Line line = make_line(p);
@@ -910,18 +887,18 @@ __global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, NT>::kCtas) paged_na
     if (bad && h == 0 && s0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
 
     // start the first stages, then the queries
-    const int mine = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
+    const int mine = s1 - s0 > team ? (s1 - s0 - team + kTeams - 1) / kTeams : 0;
     StagePages nxt;
     int base, end;
     auto find = [&](int i) {
-      stage_range(span, s0 + warp + i * kWarps, base, end);
+      stage_range(span, s0 + team + i * kTeams, base, end);
       nxt = stage_pages(p, table, base, end, magic);
     };
     if (mine > 0) find(0);
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) {
       if (i < mine) {
-        issue_stage<D, 32>(p, ring + i * kBytes, nxt, h, base, end, lane);
+        issue_stage<D, GW * 32>(p, ring + i * kBytes, nxt, h, base, end, me);
         if (i + 1 < mine) find(i + 1);
       }
       cp_commit();
@@ -929,36 +906,34 @@ __global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, NT>::kCtas) paged_na
     Rows<D, NT> R;
     Queries<D, NT> Q;
     R.clear();
-    load_rows<D, NT>(p, Q, R, qmem, seq.t0, h, 0, rows, pos0, warp == 0);
-    if (!Queries<D, NT>::kRegs) __syncthreads();
+    load_rows<D, NT>(p, Q, R, seq.t0, h, 8 * NT * member, rows, pos0);
 
     int slot_in = kRing - 1, slot_out = 0;
     for (int i = 0; i < mine; ++i) {
       cp_wait<kRing - 2>();
-      __syncwarp();
+      team_sync<GW>();  // the stage is there, and the team is done with the one before
       if (i + kRing - 1 < mine) {
-        issue_stage<D, 32>(p, ring + slot_in * kBytes, nxt, h, base, end, lane);
+        issue_stage<D, GW * 32>(p, ring + slot_in * kBytes, nxt, h, base, end, me);
         if (i + kRing < mine) find(i + kRing);
       }
       cp_commit();
       int sb, se;
-      stage_range(span, s0 + warp + i * kWarps, sb, se);
-      do_stage<D, INT8, NT, FINE>(p, ring + slot_out * kBytes, Q, R, sb);
-      __syncwarp();
+      stage_range(span, s0 + team + i * kTeams, sb, se);
+      if (sb <= R.pos_max) do_stage<D, INT8, NT, FINE>(p, ring + slot_out * kBytes, Q, R, sb);
       slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
       slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
     }
     cp_wait<0>();
     finish_sums<D, NT>(R);
 
-    // Join the warps through the rings' memory: [warp][row][D outputs, m, l, ref].
+    // Join the teams through the rings' memory: [team][row][D outputs, m, l, ref].
     __syncthreads();
     float* body = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float* e = body + (warp * kRows + 8 * n + 2 * t + c) * kRowFloats;
+        float* e = body + (team * kRows + 8 * (NT * member + n) + 2 * t + c) * kRowFloats;
         put_row<D, NT>(R, n, c, 1.f, e);
         if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c], e[D + 2] = pow2_of(R.ref);
       }
@@ -968,17 +943,17 @@ __global__ void __launch_bounds__(kWarps * 32, NarrowGeo<D, NT>::kCtas) paged_na
       const float* e = body + row * kRowFloats;
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, e[w * kRows * kRowFloats + D]);
-      float l = 0.f, f[kWarps];
+      for (int w = 0; w < kTeams; ++w) m = fmaxf(m, e[w * kRows * kRowFloats + D]);
+      float l = 0.f, f[kTeams];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kTeams; ++w) {
         f[w] = m == -INFINITY ? 0.f : exp2_fast(e[w * kRows * kRowFloats + D] - m);
         l += e[w * kRows * kRowFloats + D + 1] * f[w];
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kTeams; ++w) {
         const float4 o = *reinterpret_cast<const float4*>(e + w * kRows * kRowFloats + c);
         const float k = f[w] * inv * e[w * kRows * kRowFloats + D + 2];
         y.x += o.x * k, y.y += o.y * k, y.z += o.z * k, y.w += o.w * k;
@@ -1103,7 +1078,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
 
 // ---- the wide form: many rows a KV head --------------------------------------------------------------
 //
-// A CTA takes 128 rows, 32 a warp, and passes the stages its rows can see through
+// A CTA takes 64 rows, 16 a warp, and passes the stages its rows can see through
 // one shared ring; every warp converts the codes itself (the conversions run
 // beside the other warps' products).  Few row tiles over a long cache are cut
 // into n_splits parts of their stages, joined by paged_join_rows_kernel.
@@ -1111,11 +1086,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
 constexpr int kWideRing = 4;
 
 template <int D, bool INT8, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int NT = 4, kBytes = StageGeo<D>::kBytes, kRowFloats = D + 4;
+  constexpr int NT = 2, kBytes = StageGeo<D>::kBytes, kRowFloats = D + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint4* qmem = reinterpret_cast<uint4*>(smem + kWideRing * kBytes) + warp * (NT / 2) * (D / 16) * 32;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
   const int unit = blockIdx.y, b = unit / p.c.Hkv, h = unit % p.c.Hkv;
   // the tiles that see most come first
@@ -1150,7 +1124,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel
   Rows<D, NT> R;
   Queries<D, NT> Q;
   R.clear();
-  load_rows<D, NT>(p, Q, R, qmem, seq.t0, h, row0 + 32 * warp, rows, pos0, true);
+  load_rows<D, NT>(p, Q, R, seq.t0, h, row0 + 8 * NT * warp, rows, pos0);
   for (int i = s0; i < s1; ++i) {
     cp_wait<kWideRing - 2>();
     __syncthreads();  // the stage is there, and everyone is done with the one before
@@ -1178,7 +1152,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWideCtasPerSm) paged_wide_kernel
       if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c];
     }
     __syncwarp();
-    const int first = row0 + 32 * warp + 8 * n;
+    const int first = row0 + 8 * (NT * warp + n);
     for (int x = lane; x < 8 * (D / 4); x += 32) {
       const int rr = x / (D / 4), c = x % (D / 4) * 4, row = first + rr;
       if (row >= rows) break;
@@ -1232,29 +1206,29 @@ cudaError_t launch(void (*f)(A...), dim3 grid, dim3 block, size_t smem, bool cha
   return cudaLaunchKernelEx(&c, f, args...);
 }
 
-template <int D, bool INT8, int NT, bool FINE>
+template <int D, bool INT8, int NT, int GW, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
-  constexpr size_t rings = (size_t)kWarps * NarrowGeo<D, NT>::kStages * StageGeo<D>::kBytes;
-  constexpr size_t frags = Queries<D, NT>::kRegs ? 0 : (size_t)(NT / 2) * (D / 16) * 32 * sizeof(uint4);
-  constexpr size_t rows = (size_t)kWarps * 8 * NT * (D + 4) * sizeof(float);
-  constexpr size_t smem = rings + frags > rows ? rings + frags : rows;
-  cudaError_t e = launch(paged_narrow_kernel<D, INT8, NT, FINE>, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
+  constexpr int kRows = 8 * NT * GW;
+  constexpr size_t smem = (size_t)NarrowGeo<D, GW>::kTeams * NarrowGeo<D, GW>::kStages * StageGeo<D>::kBytes;
+  static_assert(smem >= (size_t)NarrowGeo<D, GW>::kTeams * kRows * (D + 4) * sizeof(float), "the joined rows fit the rings");
+  cudaError_t e = launch(paged_narrow_kernel<D, INT8, NT, GW, FINE>, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess) return e;
-  const int n = p.b.max_new * p.G < 8 * NT ? p.b.max_new * p.G : 8 * NT;
-  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, 8 * NT);
+  const int n = p.b.max_new * p.G < kRows ? p.b.max_new * p.G : kRows;
+  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, kRows);
 }
-template <int D, bool INT8>
-cudaError_t narrow(const PagedAttnParams& p, int tiles, cudaStream_t s) {
-  if (p.half)
-    return tiles == 1 ? narrow<D, INT8, 1, true>(p, s) : tiles == 2 ? narrow<D, INT8, 2, true>(p, s) : narrow<D, INT8, 4, true>(p, s);
-  return tiles == 1 ? narrow<D, INT8, 1, false>(p, s) : tiles == 2 ? narrow<D, INT8, 2, false>(p, s) : narrow<D, INT8, 4, false>(p, s);
+template <int D, bool INT8, bool FINE>
+cudaError_t narrow(const PagedAttnParams& p, int rows, cudaStream_t s) {
+  switch (rows) {
+    case 8: return narrow<D, INT8, 1, 1, FINE>(p, s);
+    case 16: return narrow<D, INT8, 2, 1, FINE>(p, s);
+    case 32: return narrow<D, INT8, 2, 2, FINE>(p, s);
+    default: return narrow<D, INT8, 2, 4, FINE>(p, s);
+  }
 }
 
 template <int D, bool INT8, bool FINE>
 cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
-  constexpr size_t ring = (size_t)kWideRing * StageGeo<D>::kBytes;
-  constexpr size_t frags = (size_t)kWarps * 2 * (D / 16) * 32 * sizeof(uint4);
-  constexpr size_t smem = ring + frags;
+  constexpr size_t smem = (size_t)kWideRing * StageGeo<D>::kBytes;
   static_assert(smem >= (size_t)kWarps * 8 * (D + 4) * sizeof(float), "the rows that leave fit");
   const int64_t tiles = ((int64_t)p.b.max_new * p.G + kWideRows - 1) / kWideRows;
   cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
@@ -1274,9 +1248,13 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
                 dim3(threads), 0, false, s, p);
 }
 
-cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int tiles, cudaStream_t s) {
-  if (D == 128) return int8 ? narrow<128, true>(p, tiles, s) : narrow<128, false>(p, tiles, s);
-  return int8 ? narrow<64, true>(p, tiles, s) : narrow<64, false>(p, tiles, s);
+cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int rows, cudaStream_t s) {
+  if (p.half) {
+    if (D == 128) return int8 ? narrow<128, true, true>(p, rows, s) : narrow<128, false, true>(p, rows, s);
+    return int8 ? narrow<64, true, true>(p, rows, s) : narrow<64, false, true>(p, rows, s);
+  }
+  if (D == 128) return int8 ? narrow<128, true, false>(p, rows, s) : narrow<128, false, false>(p, rows, s);
+  return int8 ? narrow<64, true, false>(p, rows, s) : narrow<64, false, false>(p, rows, s);
 }
 
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s) {

@@ -56,14 +56,13 @@ struct PagedAttnParams {
 };
 
 // Rows (new tokens x heads of a group) of one sequence and KV head that the
-// narrow form takes: 1, 2 or 4 matrix tiles of 8 rows.
-constexpr int kNarrowRows = 32;
-constexpr int kWideRows = 128;  // rows of a CTA of the wide form
-constexpr int kWideCtasPerSm = 2;
-constexpr int narrow_ctas_per_sm(int tiles) { return tiles <= 2 ? 3 : 2; }
+// narrow form takes, and those of a CTA of the wide form.
+constexpr int kNarrowRows = 64;
+constexpr int kWideRows = 64;
+constexpr int kCtasPerSm = 3;
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
-cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int tiles, cudaStream_t s);
+cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int rows, cudaStream_t s);
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 
 }  // namespace hyb

@@ -42,6 +42,8 @@ from ._abi import (  # noqa: F401
     hyb_attn_paged_append,
     hyb_attn_paged_workspace_size,
     hyb_attn_paged_attend,
+    hyb_attn_delta_state,
+    hyb_attn_delta_run,
     hyb_attn_destroy,
     hyb_attn_strerror,
     hyb_attn_last_cuda_error,
@@ -54,6 +56,7 @@ from ._abi import (  # noqa: F401
     HYB_STATUS_NAN_SCORE,
     HYB_STATUS_BAD_PAGE,
     HYB_STATUS_BAD_LENGTH,
+    HYB_STATUS_BAD_SLOT,
     HYB_CODE_E4M3,
     HYB_CODE_INT8,
     HYB_TYPE_BF16,
@@ -61,4 +64,5 @@ from ._abi import (  # noqa: F401
     HYB_TEST_WITHHOLD_SCORES,
 )
 from .layer import HybridAttentionLayer, make_config  # noqa: F401
+from .delta import GatedDeltaState  # noqa: F401
 from .paged import PagedKVCache  # noqa: F401

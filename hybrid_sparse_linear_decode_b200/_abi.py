@@ -30,6 +30,7 @@ HYB_STATUS_TIMEOUT = 0x8
 HYB_STATUS_NAN_SCORE = 0x10
 HYB_STATUS_BAD_PAGE = 0x20
 HYB_STATUS_BAD_LENGTH = 0x40
+HYB_STATUS_BAD_SLOT = 0x80
 
 HYB_CODE_E4M3 = 0
 HYB_CODE_INT8 = 1
@@ -73,6 +74,11 @@ class hyb_attn_paged_batch(ctypes.Structure):
                 ("n_new", c_i32), ("max_new", c_i32), ("max_len", c_i32), ("status", c_vp)]
 
 
+class hyb_attn_delta_state(ctypes.Structure):
+    _fields_ = [("state", c_vp), ("n_slots", c_i32), ("n_k_heads", c_i32), ("n_v_heads", c_i32), ("key_dim", c_i32),
+                ("value_dim", c_i32)]
+
+
 # (name, restype, argtypes) of every entry point declared in include/hyb_attn.h
 SIGNATURES = [
     ("hyb_attn_query_sizes", ctypes.c_int, [ctypes.POINTER(hyb_attn_config), ctypes.POINTER(hyb_attn_sizes)]),
@@ -114,6 +120,8 @@ SIGNATURES = [
     ("hyb_attn_paged_attend", ctypes.c_int, [ctypes.POINTER(hyb_attn_paged_cache), ctypes.POINTER(hyb_attn_paged_batch),
                                              c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i32, c_i32, c_f32, c_vp,
                                              c_sz, c_vp]),
+    ("hyb_attn_delta_run", ctypes.c_int, [ctypes.POINTER(hyb_attn_delta_state), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
+                                          c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_i32, c_f32, c_vp, c_vp]),
     ("hyb_attn_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("hyb_attn_last_cuda_error", ctypes.c_char_p, []),
 ]
@@ -326,3 +334,11 @@ def hyb_attn_paged_attend(cache: hyb_attn_paged_cache, batch: hyb_attn_paged_bat
            load_library().hyb_attn_paged_attend(ctypes.byref(cache), ctypes.byref(batch), type, q, q_stride, out,
                                                 out_stride, lse, n_q_heads, window, n_sink, scale, workspace,
                                                 workspace_bytes, stream))
+
+
+def hyb_attn_delta_run(state: hyb_attn_delta_state, q: int, q_stride: int, k: int, k_stride: int, v: int, v_stride: int,
+                       g: int, beta: int, out: int, out_stride: int, cu_new: int, slots, batch: int, n_new: int,
+                       max_new: int, scale: float, status, stream: int) -> None:
+    _check("hyb_attn_delta_run",
+           load_library().hyb_attn_delta_run(ctypes.byref(state), q, q_stride, k, k_stride, v, v_stride, g, beta, out,
+                                             out_stride, cu_new, slots, batch, n_new, max_new, scale, status, stream))

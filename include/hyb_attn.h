@@ -73,8 +73,9 @@ extern "C" {
 #define HYB_STATUS_BAD_SELECTION 0x4u  /* a caller-given block index was out of range (skipped) */
 #define HYB_STATUS_TIMEOUT       0x8u  /* a bounded wait inside a kernel gave up */
 #define HYB_STATUS_NAN_SCORE     0x10u /* a block score was NaN (ranked last) */
-/* bits of the caller's own status word (paged cache calls) */
+/* bits of the caller's own status word (paged cache and delta rule calls) */
 #define HYB_STATUS_BAD_PAGE      0x20u /* a page index outside the cache (its tokens are skipped) */
+#define HYB_STATUS_BAD_SLOT      0x80u /* a state index outside the states, other than -1 (sequence skipped) */
 #define HYB_STATUS_BAD_LENGTH    0x40u /* lengths or row ranges outside what the call was told (held to it) */
 
 /* ---- failure injection for tests (hyb_attn_set_test_flags) ---------------- */
@@ -515,6 +516,42 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
                           const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
                           int32_t n_q_heads, int32_t window, int32_t n_sink, float scale, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
+
+/* ===========================================================================
+ * Gated delta rule
+ *
+ * The linear state above adds every evicted token's k v^T for good.  A linear
+ * layer that forgets keeps S [key_dim][value_dim] per sequence and head, and for
+ * each token, with a = exp(g):
+ *   S := a S;   S := S + k (beta (v - S^T k))^T;   o = scale S^T q.
+ * ======================================================================== */
+typedef struct hyb_attn_delta_state {
+  float* state;         /* fp32 [n_slots][n_v_heads][key_dim][value_dim], 16-byte aligned */
+  int32_t n_slots;
+  int32_t n_k_heads;    /* of q and k; head i of v uses head i / (n_v_heads / n_k_heads) */
+  int32_t n_v_heads;    /* of v, g, beta, out; a multiple of n_k_heads */
+  int32_t key_dim;      /* 64 or 128 */
+  int32_t value_dim;    /* 64 or 128 */
+} hyb_attn_delta_state;
+
+/* Take every sequence's new tokens through the rule, from its state to its new
+ * state (in place).  Sequence b owns rows [cu_new[b], cu_new[b + 1]) and state
+ * slots[b] (slots NULL: state b).  A slot of -1 skips the sequence: its rows and
+ * every state are left as they were; other slots outside the states do so too
+ * and set HYB_STATUS_BAD_SLOT.  Two sequences of one call never share a slot.
+ *   q, k   bf16 [n_new] rows of [n_k_heads][key_dim]; v: of [n_v_heads][value_dim];
+ *          strides in elements, multiples of 8
+ *   g, beta fp32 [n_new][n_v_heads]; g <= 0 is a decay's logarithm, -inf forgets
+ *          all;  beta the learning rate.  k is taken as it is: for the rule to be
+ *          stable |k| <= 1 and 0 <= beta <= 1 (or beta |k|^2 < 2).
+ *   out    bf16 rows of [n_v_heads][value_dim]
+ * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
+ * the tokens one by one with the state in registers; long ones in chunks of 64
+ * by matrix products.  One launch, no workspace.  Errors: HYB_EINVAL, HYB_ECUDA. */
+int hyb_attn_delta_run(const hyb_attn_delta_state* state, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const float* g, const float* beta,
+                       void* out, int64_t out_stride, const int32_t* cu_new, const int32_t* slots, int32_t batch,
+                       int32_t n_new, int32_t max_new, float scale, uint32_t* status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -2,6 +2,7 @@
 
 Objects are compiled in parallel under ``_build/`` and linked with the static
 CUDA runtime, so the library carries its own runtime and needs no JIT cache.
+``_binding.so`` (the calls that take PyTorch tensors) is linked against it.
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhyb_attn.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "api_delta.cu", "api_paged.cu", "k_delta.cu", "k_fused.cu", "k_multi.cu", "k_paged.cu", "k_select.cu", "k_state.cu"]
 HEADERS = ["hyb_device.cuh", "hyb_internal.h", "k_common.cuh", "k_delta.h", "k_paged.h", "k_select.h"]
@@ -31,6 +33,33 @@ def _stale(out: str, deps) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def compile_binding(force: bool) -> str:
+    """The compiled calls from PyTorch tensors (host code only)."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD_DIR, "binding.o")
+    if force or _stale(obj, [src, os.path.join(ROOT, "include", "hyb_attn.h")]):
+        includes = [f"-I{p}" for p in cpp_extension.include_paths()]
+        includes += [f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.dirname(os.path.dirname(nvcc()))}/include"]
+        r = subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-DTORCH_API_INCLUDE_EXTENSION_H",
+                            *includes, "-c", src, "-o", obj], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{src}:\n{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    from torch.utils import cpp_extension
+    libs = [p for d in cpp_extension.library_paths() for p in (f"-L{d}", f"-Wl,-rpath,{d}")]
+    r = subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING + ".tmp", obj, f"-L{HERE}", "-l:libhyb_attn.so",
+                        "-Wl,-rpath,$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -50,8 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        binding = ex.submit(compile_binding, force)
         logs = list(ex.map(compile_one, srcs, objs))
+        binding = binding.result()
     if verbose:
         for lg in logs:
             if lg:
@@ -62,6 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    if force or _stale(BINDING, [binding]):
+        link_binding(binding)
     return LIB
 
 

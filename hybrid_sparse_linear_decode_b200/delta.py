@@ -5,10 +5,12 @@ PyTorch is used for device memory and streams only; the work is the library's.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _abi as A
-from ._tensors import need, rows_of, run_on, vector_of
+from ._tensors import binding, need, on_stream
 
 
 class GatedDeltaState:
@@ -42,6 +44,8 @@ class GatedDeltaState:
         self._status = torch.zeros(1, dtype=torch.int32, device=state.device)
         self._status_at = self._status.data_ptr()
         self._c = A.hyb_attn_delta_state(state.data_ptr(), self.n_slots, n_k_heads, self.n_v_heads, self.key_dim, self.value_dim)
+        self._c_at = ctypes.addressof(self._c)
+        self._calls = binding()
 
     def run(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, cu: torch.Tensor,
             max_new: int, slots: torch.Tensor | None = None, scale: float = 0.0, out: torch.Tensor | None = None,
@@ -50,34 +54,10 @@ class GatedDeltaState:
         state ``slots[b]`` (int32, device; default b; -1: the sequence is skipped, its rows stay as they were); ``max_new``
         bounds the rows of one sequence.  q, k [rows, n_k_heads, key_dim], v [rows, n_v_heads, value_dim] bf16; g, beta
         [rows, n_v_heads] fp32.  Returns [rows, n_v_heads, value_dim] bf16."""
-        index, dtype = self._index, torch.bfloat16
-        Hv, dv = self.n_v_heads, self.value_dim
-        qs = rows_of(q, "q", self.n_k_heads, self.key_dim, index, dtype)
-        ks = rows_of(k, "k", self.n_k_heads, self.key_dim, index, dtype)
-        vs = rows_of(v, "v", Hv, dv, index, dtype)
-        n = q.shape[0]
-        need(k.shape[0] == n and v.shape[0] == n, "q, k and v have as many rows")
-        for t, name in ((g, "g"), (beta, "beta")):
-            if t.dtype is not torch.float32 or t.shape != (n, Hv) or t.get_device() != index or not t.is_contiguous():
-                raise ValueError(f"{name} has to be a contiguous fp32 [{n}, {Hv}] tensor on {self.device}")
-        need(cu.dim() == 1 and cu.shape[0] >= 2, "cu is [B + 1]")
-        B = cu.shape[0] - 1
-        need(max_new >= 1 or n == 0, "max_new is at least 1")
-        cu_at = vector_of(cu, "cu", torch.int32, B + 1, index)
-        slots_at = None if slots is None else vector_of(slots, "slots", torch.int32, B, index)
-        os = Hv * dv
-        if out is not None:
-            os = rows_of(out, "out", Hv, dv, index, dtype)
-            need(out.shape[0] == n, "out has as many rows as q")
-
-        def call(handle):
-            to = q.new_empty((n, Hv, dv)) if out is None else out
-            A.hyb_attn_delta_run(self._c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), beta.data_ptr(),
-                                 to.data_ptr(), os, cu_at, slots_at, B, n, max_new if max_new < n else n, scale,
-                                 self._status_at, handle)
-            return to
-
-        return run_on(index, stream, call)
+        if stream is not None:
+            with on_stream(stream, self.device):
+                return self.run(q, k, v, g, beta, cu, max_new, slots, scale, out)
+        return self._calls.delta_run(self._c_at, self._index, self._status_at, q, k, v, g, beta, cu, max_new, slots, scale, out)
 
     def status(self, clear: bool = False) -> int:
         """The HYB_STATUS_* bits raised by these states' calls so far (waits for them)."""

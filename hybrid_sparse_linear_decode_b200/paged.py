@@ -5,13 +5,14 @@ PyTorch is used for device memory and streams only; the work is the library's.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _abi as A
-from ._tensors import need, rows_of, run_on, vector_of
+from ._tensors import binding, need, on_stream
 
 _CODES = {torch.float8_e4m3fn: A.HYB_CODE_E4M3, torch.int8: A.HYB_CODE_INT8}
-_TYPES = {torch.bfloat16: A.HYB_TYPE_BF16, torch.float16: A.HYB_TYPE_FP16}
 
 
 class PagedKVCache:
@@ -57,19 +58,9 @@ class PagedKVCache:
         self._index = k.get_device()
         self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._status_at = self._status.data_ptr()
-        self._sizes = {}  # workspace bytes by the limits that they follow from
         self._c = A.hyb_attn_paged_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), *k.shape, _CODES[k.dtype])
-
-    def _batch(self, cu, kv_lens, page_table, n_new, max_new, max_len) -> A.hyb_attn_paged_batch:
-        index = self._index
-        if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != index
-                or not page_table.is_contiguous()):
-            raise ValueError(f"page_table has to be a contiguous int32 [B, pages] tensor on {self.device}")
-        B, pages = page_table.shape
-        need(max_new >= 1 or n_new == 0, "max_new is at least 1")
-        return A.hyb_attn_paged_batch(page_table.data_ptr(), vector_of(cu, "cu", torch.int32, B + 1, index),
-                                      vector_of(kv_lens, "kv_lens", torch.int32, B, index), B, pages, n_new,
-                                      max_new if max_new < n_new else n_new, max_len, self._status_at)
+        self._c_at = ctypes.addressof(self._c)
+        self._calls = binding()
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
                max_new: int, rope: torch.Tensor | None = None, interleaved: bool = False, q: torch.Tensor | None = None,
@@ -77,41 +68,11 @@ class PagedKVCache:
         """Append a step's tokens: k, v [rows, n_kv_heads, d] (bf16 or fp16), keys rotated by ``rope`` (fp32
         [positions, rot_dim]: cosines, then sines).  With ``q`` [rows, n_q_heads, d] returns the queries rotated alike
         (into ``q_out``, which may be ``q``)."""
-        index, d, dtype = self._index, self.head_dim, k.dtype
-        if dtype not in _TYPES:
-            raise ValueError(f"k is {dtype}, not bfloat16 or float16")
-        ks = rows_of(k, "k", self.n_kv_heads, d, index)
-        vs = rows_of(v, "v", self.n_kv_heads, d, index, dtype)
-        n = k.shape[0]
-        need(v.shape[0] == n, "k and v have as many rows")
-        n_pos = rot = heads = qs = qo = 0
-        rope_at = q_at = qo_at = None
-        if rope is not None:
-            if rope.dim() != 2 or rope.dtype is not torch.float32 or rope.get_device() != index or not rope.is_contiguous():
-                raise ValueError("rope has to be a contiguous fp32 [positions, rot_dim] tensor on the cache's device")
-            n_pos, rot = rope.shape
-            rope_at = rope.data_ptr()
-        if q is not None:
-            need(q.dim() == 3 and q.shape[0] == n, "q is [rows, n_q_heads, head_dim], with as many rows as k")
-            heads, q_at = q.shape[1], q.data_ptr()
-            qs = rows_of(q, "q", heads, d, index, dtype)
-            if q_out is not None:
-                qo, qo_at = rows_of(q_out, "q_out", heads, d, index, dtype), q_out.data_ptr()
-                need(q_out.shape[0] == n, "q_out has as many rows as q")
-        else:
-            need(q_out is None, "q_out without q")
-        b = self._batch(cu, kv_lens, page_table, n, max_new, 0)
-
-        def call(handle):
-            to, to_at, to_stride = q_out, qo_at, qo
-            if q is not None and to is None:
-                to = q.new_empty((n, heads, d))
-                to_at, to_stride = to.data_ptr(), heads * d
-            A.hyb_attn_paged_append(self._c, b, _TYPES[dtype], k.data_ptr(), ks, v.data_ptr(), vs, rope_at, n_pos, rot,
-                                    interleaved, q_at, qs, to_at, to_stride, heads, handle)
-            return to
-
-        return run_on(index, stream, call)
+        if stream is not None:
+            with on_stream(stream, self.device):
+                return self.append(k, v, cu, kv_lens, page_table, max_new, rope, interleaved, q, q_out)
+        return self._calls.paged_append(self._c_at, self._index, self._status_at, k, v, cu, kv_lens, page_table, max_new, rope,
+                                        interleaved, q, q_out)
 
     def attend(self, q: torch.Tensor, cu: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, max_new: int,
                max_len: int, window: int = 0, n_sink: int = 0, scale: float = 0.0, out: torch.Tensor | None = None,
@@ -120,33 +81,11 @@ class PagedKVCache:
         [rows, n_q_heads, d] in q's type, with ``return_lse`` also the fp32 [rows, n_q_heads] logarithms of the softmax
         sums.  ``window`` > 0 hides positions t - window and before, but for the first ``n_sink``.  Rows behind
         the last sequence are left as they were (in new tensors: not written)."""
-        index, d, dtype = self._index, self.head_dim, q.dtype
-        if dtype not in _TYPES or q.dim() != 3:
-            raise ValueError("q has to be [rows, n_q_heads, head_dim], bfloat16 or float16")
-        n, heads, _ = q.shape
-        qs = rows_of(q, "q", heads, d, index)
-        b = self._batch(cu, kv_lens, page_table, n, max_new, max_len)
-        key = (n, heads, b.max_new, max_len, b.batch, b.table_stride)
-        size = self._sizes.get(key)
-        if size is None:
-            if len(self._sizes) > 256:
-                self._sizes.clear()
-            size = self._sizes[key] = A.hyb_attn_paged_workspace_size(self._c, b, heads)
-        os = heads * d
-        if out is not None:
-            os = rows_of(out, "out", heads, d, index, dtype)
-            need(out.shape[0] == n, "out has as many rows as q")
-
-        def call(handle):
-            to = q.new_empty((n, heads, d)) if out is None else out
-            lse = q.new_empty((n, heads), dtype=torch.float32) if return_lse else None
-            ws = q.new_empty(size, dtype=torch.uint8) if size else None
-            A.hyb_attn_paged_attend(self._c, b, _TYPES[dtype], q.data_ptr(), qs, to.data_ptr(), os,
-                                    lse.data_ptr() if return_lse else None, heads, window, n_sink, scale,
-                                    ws.data_ptr() if size else None, size, handle)
-            return (to, lse) if return_lse else to
-
-        return run_on(index, stream, call)
+        if stream is not None:
+            with on_stream(stream, self.device):
+                return self.attend(q, cu, kv_lens, page_table, max_new, max_len, window, n_sink, scale, out, return_lse)
+        return self._calls.paged_attend(self._c_at, self._index, self._status_at, q, cu, kv_lens, page_table, max_new, max_len,
+                                        window, n_sink, scale, out, return_lse)
 
     def status(self, clear: bool = False) -> int:
         """The HYB_STATUS_* bits raised by this cache's calls so far (waits for them)."""

@@ -43,8 +43,8 @@ def compile_binding(force: bool) -> str:
     src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD_DIR, "binding.o")
     if force or _stale(obj, [src, os.path.join(ROOT, "include", "hyb_attn.h")]):
         includes = [f"-I{p}" for p in cpp_extension.include_paths()]
-        includes += [f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.dirname(os.path.dirname(nvcc()))}/include"]
-        r = subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-DTORCH_API_INCLUDE_EXTENSION_H",
+        includes.append(f"-I{sysconfig.get_paths()['include']}")
+        r = subprocess.run([nvcc(), "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-DTORCH_API_INCLUDE_EXTENSION_H",
                             *includes, "-c", src, "-o", obj], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{src}:\n{r.stderr}")
@@ -53,10 +53,10 @@ def compile_binding(force: bool) -> str:
 
 def link_binding(obj: str) -> None:
     from torch.utils import cpp_extension
-    libs = [p for d in cpp_extension.library_paths() for p in (f"-L{d}", f"-Wl,-rpath,{d}")]
-    r = subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", BINDING + ".tmp", obj, f"-L{HERE}", "-l:libhyb_attn.so",
-                        "-Wl,-rpath,$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"],
-                       capture_output=True, text=True)
+    libs = [p for d in cpp_extension.library_paths() for p in (f"-L{d}", "-Xlinker", f"-rpath={d}")]
+    r = subprocess.run([nvcc(), "-shared", "-o", BINDING + ".tmp", obj, f"-L{HERE}", "-l:libhyb_attn.so", "-Xlinker",
+                        "-rpath=$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-cudart",
+                        "none"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)

@@ -122,10 +122,15 @@ __device__ __forceinline__ Runs lane_runs(int j, int rot, bool interleaved) {
   r.c1 = turned && !interleaved ? rot / 2 + 8 * j : 16 * j + 8;
   return r;
 }
-__device__ __forceinline__ void load_runs(const uint16_t* row, const Runs& r, bool half, float* x) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + r.c0));
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(row + r.c1));
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// The runs as they are loaded, and as values.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw load_runs(const uint16_t* row, const Runs& r) {
+  return Raw{__ldg(reinterpret_cast<const uint4*>(row + r.c0)), __ldg(reinterpret_cast<const uint4*>(row + r.c1))};
+}
+__device__ __forceinline__ void to_values(const Raw& raw, bool half, float* x) {
+  const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = in_lo(w[i], half);
@@ -175,6 +180,12 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
     const int hg = (int)(rest % groups);
     const int64_t t = rest / groups;
     if (t >= p.b.n_new) return;
+    const Runs r = lane_runs(j, p.rot, INTERLEAVED);
+    const int heads = min(4, p.Hq - hg * 4);
+    Raw raw[4];  // under way before the token's sequence is known
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      if (h < heads) raw[h] = load_runs(p.q + t * p.q_stride + (int64_t)(hg * 4 + h) * p.D, r);
     // the token's sequence: the last b with cu[b] <= t
     int lo = 0, hi = p.b.B;
     while (hi - lo > 1) {
@@ -184,25 +195,21 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
     bool bad;
     const Seq s = read_seq(p.b, lo, P, &bad);
     if (t < s.t0 || t >= s.t0 + s.n) return;  // a row behind the last sequence
-    const Runs r = lane_runs(j, p.rot, INTERLEAVED);
     Angles a;
     if (r.angle >= 0) {
       const int pos = s.len - s.n + (int)(t - s.t0);
       if (pos < 0 || pos >= p.n_pos) raise(p.status, HYB_STATUS_BAD_LENGTH);
       load_angles(a, p.rope + (int64_t)min(max(pos, 0), p.n_pos - 1) * p.rot, p.rot, r.angle);
     }
-    const int heads = min(4, p.Hq - hg * 4);
-    float x[4][16];
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      if (h < heads) load_runs(p.q + t * p.q_stride + (int64_t)(hg * 4 + h) * p.D, r, half, x[h]);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       if (h >= heads) break;
-      if (r.angle >= 0) turn<false>(x[h], a, INTERLEAVED);
+      float x[16];
+      to_values(raw[h], half, x);
+      if (r.angle >= 0) turn<false>(x, a, INTERLEAVED);
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_out(x[h][2 * i], x[h][2 * i + 1], half);
+      for (int i = 0; i < 8; ++i) w[i] = pack_out(x[2 * i], x[2 * i + 1], half);
       uint16_t* row = p.q_out + t * p.qo_stride + (int64_t)(hg * 4 + h) * p.D;
       *reinterpret_cast<uint4*>(row + r.c0) = make_uint4(w[0], w[1], w[2], w[3]);
       *reinterpret_cast<uint4*>(row + r.c1) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -227,6 +234,16 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
   const int pg = first / P + pi;  // page of the sequence
   const int lo = max(pg * P, first), hi = (int)min((int64_t)(pg + 1) * P, (int64_t)s.len);
   if (lo >= hi) return;
+  const int j = threadIdx.x % lanes, row0 = threadIdx.x / lanes, step = blockDim.x / lanes;
+  const Runs r = lane_runs(j, values ? 0 : p.rot, INTERLEAVED);
+  const uint16_t* in = values ? p.v : p.k;
+  const int64_t stride = values ? p.v_stride : p.k_stride;
+  Raw raw[kAppendRows];  // under way before the page is known
+#pragma unroll
+  for (int i = 0; i < kAppendRows; ++i) {
+    const int pos = lo + row0 + i * step;
+    if (pos < hi) raw[i] = load_runs(in + (int64_t)(s.t0 + pos - start) * stride + (int64_t)h * p.D, r);
+  }
   const int page = p.b.table[(int64_t)b * p.b.mp + pg];
   if (page < 0 || page >= p.c.n_pages) {
     if (threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_PAGE);
@@ -237,22 +254,14 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
   const int older = lo - pg * P;  // tokens that the page held before
   const float was = older > 0 ? *scale_at : 0.f;
 
-  const int j = threadIdx.x % lanes, row0 = threadIdx.x / lanes, step = blockDim.x / lanes;
-  const Runs r = lane_runs(j, values ? 0 : p.rot, INTERLEAVED);
-  const uint16_t* in = values ? p.v : p.k;
-  const int64_t stride = values ? p.v_stride : p.k_stride;
   float x[kAppendRows][16];
   float amax = 0.f;
   bool odd = false;  // an infinite or NaN value among them
 #pragma unroll
   for (int i = 0; i < kAppendRows; ++i) {
     const int pos = lo + row0 + i * step;
-    if (pos < hi) load_runs(in + (int64_t)(s.t0 + pos - start) * stride + (int64_t)h * p.D, r, half, x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    const int pos = lo + row0 + i * step;
     if (pos >= hi) continue;
+    to_values(raw[i], half, x[i]);
     if (r.angle >= 0) {
       Angles a;
       if (pos >= p.n_pos) raise(p.status, HYB_STATUS_BAD_LENGTH);

@@ -56,31 +56,42 @@ bool rows_ok(const void* p, int64_t stride, int64_t heads, int d, int64_t unit) 
 }
 
 struct Plan {
-  int rows;      // of the narrow form (8, 16, 32 or 64); 0 selects the wide form
-  int n_cta;     // narrow
-  int n_splits;  // wide
+  enum Form { kNarrow, kWide, kMma } form;
+  int rows;      // of the line's units: narrow 8, 16, 32 or 64, mma 128; 0 with splits
+  int n_cta;     // line
+  int n_splits;  // otherwise
   size_t bytes;
 };
 
-// Narrow up to 64 rows a KV head, 16 a warp.  Every CTA gets at least a stage for each of its warps, as many CTAs as the SMs hold at most.
-// Wide: as many parts of each row tile's stages as fill the SMs, each of at least 8 stages.
-Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink) {
+// Up to kNarrowMost rows a KV head: narrow, 8 or 16 rows a warp, bound by the codes' bytes.  More: bf16 on tcgen05, in
+// whose 128 rows one conversion of the codes serves all; fp16, whose weights go in as two parts, on the warps' own
+// products (narrow up to 64 rows, then wide).  While a sequence's rows fit one tile the CTAs share the line of all
+// tiles; more rows, and few row tiles, cut each row tile's tokens into as many parts as fill the SMs, each of at least
+// kLeastTokens.
+constexpr int kNarrowMost = 16;
+constexpr int kLeastTokens = 256;
+
+Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink, int type) {
   Plan p{};
   const int G = Hq / c->n_kv_heads;
   const int64_t units = (int64_t)b->batch * c->n_kv_heads;
   const int64_t rows = (int64_t)b->max_new * G;
   int64_t len = std::min<int64_t>(b->max_len, (int64_t)b->table_stride * c->page_size);
   if (window > 0) len = std::min<int64_t>(len, (int64_t)window + sink + b->max_new + 64);
-  const int64_t stages = std::max<int64_t>(1, (len + 31) / 32);
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
-  if (rows <= kNarrowRows) {
-    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * kCtasPerSm, (units * stages + 3) / 4));
+  const bool mma = rows > kNarrowMost && type == HYB_TYPE_BF16;
+  p.form = mma ? Plan::kMma : rows <= kNarrowRows ? Plan::kNarrow : Plan::kWide;
+  const int tile = mma ? kMmaRows : kWideRows;
+  if (p.form == Plan::kNarrow || (mma && rows <= tile)) {
+    const int64_t stage = mma ? 128 : 32, warps = mma ? 1 : 4;
+    const int64_t stages = std::max<int64_t>(1, (len + stage - 1) / stage);
+    p.rows = mma ? tile : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * (mma ? kMmaCtasPerSm : kCtasPerSm), (units * stages + warps - 1) / warps));
     p.bytes = (size_t)2 * p.n_cta * p.rows * row_bytes;
   } else {
-    const int64_t tiles = units * ((rows + kWideRows - 1) / kWideRows);
-    int64_t n = tiles >= kSms * kCtasPerSm ? 1 : (kSms * kCtasPerSm + tiles - 1) / tiles;
-    n = std::max<int64_t>(1, std::min<int64_t>({n, stages / 8, 64}));
+    const int64_t tiles = units * ((rows + tile - 1) / tile), all = kSms * (mma ? kMmaCtasPerSm : kCtasPerSm);
+    int64_t n = tiles >= all ? 1 : (all + tiles - 1) / tiles;
+    n = std::max<int64_t>(1, std::min<int64_t>({n, len / kLeastTokens, 64}));
     if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
     p.n_splits = (int)n;
     p.bytes = n > 1 ? (size_t)n * b->n_new * Hq * row_bytes : 0;
@@ -140,7 +151,7 @@ int hyb_attn_paged_append(const hyb_attn_paged_cache* cache, const hyb_attn_page
 size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch,
                                      int32_t n_q_heads) {
   if (!shapes_ok(cache, batch) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || batch->n_new == 0) return 0;
-  return make_plan(cache, batch, n_q_heads, 0, 0).bytes;
+  return std::max(make_plan(cache, batch, n_q_heads, 0, 0, HYB_TYPE_BF16).bytes, make_plan(cache, batch, n_q_heads, 0, 0, HYB_TYPE_FP16).bytes);
 }
 
 int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
@@ -157,7 +168,7 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   if (!rows_ok(q, q_stride, n_q_heads, d, 8) || !rows_ok(out, out_stride, n_q_heads, d, 4)) return HYB_EINVAL;
   if (lse != nullptr && !aligned(lse, 4)) return HYB_EINVAL;
   if ((int64_t)batch->max_new * (n_q_heads / cache->n_kv_heads) > ((int64_t)1 << 30)) return HYB_EINVAL;
-  const Plan plan = make_plan(cache, batch, n_q_heads, window, n_sink);
+  const Plan plan = make_plan(cache, batch, n_q_heads, window, n_sink, type);
   if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes)) return HYB_ESCRATCH;
   if (plan.bytes > 0 && !aligned(workspace, 16)) return HYB_EINVAL;
   PagedAttnParams p{};
@@ -175,11 +186,14 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   p.S = window > 0 ? n_sink : 0;
   p.scale = (scale > 0.f ? scale : 1.f / sqrtf((float)d)) * 1.44269504088896341f;
   p.n_cta = plan.n_cta;
+  p.quantum = plan.form == Plan::kMma ? 1 : 4;
   p.n_splits = plan.n_splits;
   p.ws = static_cast<float*>(workspace);
   p.status = batch->status;
   const int int8 = cache->code == HYB_CODE_INT8;
-  const cudaError_t e = plan.rows > 0 ? launch_paged_narrow(p, d, int8, plan.rows, stream) : launch_paged_wide(p, d, int8, stream);
+  const cudaError_t e = plan.form == Plan::kMma      ? launch_paged_mma(p, d, int8, stream)
+                        : plan.form == Plan::kNarrow ? launch_paged_narrow(p, d, int8, plan.rows, stream)
+                                                     : launch_paged_wide(p, d, int8, stream);
   return e == cudaSuccess ? HYB_OK : record_cuda_error(e);
 }
 

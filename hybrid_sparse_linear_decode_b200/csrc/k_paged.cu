@@ -1,357 +1,9 @@
-// Attention over the paged 8-bit cache, and the append that fills it.
-#include <cuda_fp16.h>
-
-#include <cfloat>
-
-#include "hyb_device.cuh"
-#include "k_paged.h"
+// Attention over the paged 8-bit cache.
+#include "k_paged.cuh"
 
 namespace hyb {
 namespace {
 
-__device__ __forceinline__ void raise(uint32_t* status, uint32_t bit) {
-  if (status != nullptr) atomicOr(status, bit);
-}
-
-// ---- 16-bit inputs ----------------------------------------------------------------------------
-__device__ __forceinline__ float in_lo(uint32_t w, bool half) {
-  return half ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))) : bf16_lo(w);
-}
-__device__ __forceinline__ float in_hi(uint32_t w, bool half) {
-  return half ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : bf16_hi(w);
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool half) {
-  return half ? pack_half(lo, hi) : pack_bf16(lo, hi);
-}
-
-// ---- a sequence of the step --------------------------------------------------------------------
-struct Seq {
-  int t0, n, len;  // first row, new tokens, tokens in all
-};
-
-// Reads a sequence's ranges and holds them within what the caller said: rows
-// within [0, n_new), at most max_new of them, a length within the page table.
-__device__ __forceinline__ Seq read_seq(const PagedBatch& b, int i, int P, bool* bad) {
-  Seq s;
-  const int c0 = b.cu[i], c1 = b.cu[i + 1], len = b.lens[i];
-  s.t0 = min(max(c0, 0), b.n_new);
-  const int t1 = min(max(c1, s.t0), b.n_new);
-  s.n = min(t1 - s.t0, b.max_new);
-  const int64_t cap = (int64_t)b.mp * P;
-  s.len = (int)min((int64_t)max(len, 0), cap);
-  *bad = s.t0 != c0 || s.n != c1 - c0 || s.len != len;
-  return s;
-}
-
-// ================================================================================================
-// Append
-// ================================================================================================
-//
-// One CTA takes the new tokens that fall into one page of one sequence, for one
-// KV head and for keys or values: it holds them rotated in registers (4 rows of
-// 16 channels a thread), reduces their largest magnitude, settles the page's
-// scale, rewrites the codes that the page already holds if the scale grew, and
-// writes the new codes.  So each input is read once and each code written once.
-
-constexpr int kAppendRows = 4;  // rows a thread holds
-constexpr int kRotateThreads = 256;
-constexpr int64_t kRotateApart = 1 << 17;
-
-// a * c - b * s, correctly rounded for 16-bit a and b but for ties within 2^-45:
-// the products' rounding errors are exact (fma), their difference's too (two-sum).
-__device__ __forceinline__ float diff_of_products(float a, float c, float b, float s) {
-  const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
-  const float q = __fmul_rn(b, s), qe = __fmaf_rn(b, s, -q);
-  const float d = __fsub_rn(p, q);
-  const float bb = __fsub_rn(d, p);
-  const float de = __fsub_rn(__fsub_rn(p, __fsub_rn(d, bb)), __fadd_rn(q, bb));
-  return __fadd_rn(d, __fadd_rn(de, __fsub_rn(pe, qe)));  // NaN where an input is not finite, or a product overflows
-}
-
-template <bool INT8>
-__device__ __forceinline__ float scale_for(float amax) {
-  if (INT8) return fmaxf(__fdiv_rn(amax, 127.f), 1.17549435e-38f);
-  // the smallest power of two x in [2^-126, 2^126] with amax <= 448 x:
-  // 448 = 1.75 * 2^8, so x = 2^(e - 8) or the next for amax = m 2^e, 1 <= m < 2
-  const uint32_t u = __float_as_uint(amax);
-  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = min(max(e, -126), 126);
-  return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-// Code of y (already divided by the scale, not NaN): nearest, ties to even, saturating.
-template <bool INT8>
-__device__ __forceinline__ uint32_t code2(float lo, float hi) {
-  if (INT8) {
-    const int a = __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f));
-    const int b = __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f));
-    return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8);
-  }
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <bool INT8>
-__device__ __forceinline__ uint32_t code4(const float* y, float inv) {
-  return code2<INT8>(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)) | (code2<INT8>(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)) << 16);
-}
-// The value a code stands for, without its scale (e4m3's NaN codes stay NaN).
-template <bool INT8>
-__device__ __forceinline__ float value_of(uint32_t byte) {
-  if (INT8) return (float)(int)(int8_t)byte;
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
-}
-
-// The 16 channels of a lane: two runs of 8 that hold whole pairs.  Of the first
-// rot channels, half-split pairs (i, i + rot / 2) take a run from each half;
-// interleaved pairs and the channels past rot take 16 in a row.
-struct Runs {
-  int c0, c1, angle;  // first channels of the runs; first pair, or -1 outside the rotation
-};
-__device__ __forceinline__ Runs lane_runs(int j, int rot, bool interleaved) {
-  Runs r;
-  const bool turned = j < rot / 16;
-  r.angle = turned ? 8 * j : -1;
-  r.c0 = turned && !interleaved ? 8 * j : 16 * j;
-  r.c1 = turned && !interleaved ? rot / 2 + 8 * j : 16 * j + 8;
-  return r;
-}
-// The runs as they are loaded, and as values.
-struct Raw {
-  uint4 a, b;
-};
-__device__ __forceinline__ Raw load_runs(const uint16_t* row, const Runs& r) {
-  return Raw{__ldg(reinterpret_cast<const uint4*>(row + r.c0)), __ldg(reinterpret_cast<const uint4*>(row + r.c1))};
-}
-__device__ __forceinline__ void to_values(const Raw& raw, bool half, float* x) {
-  const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = in_lo(w[i], half);
-    x[2 * i + 1] = in_hi(w[i], half);
-  }
-}
-struct Angles {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void load_angles(Angles& a, const float* row, int rot, int at) {
-  const float4* c = reinterpret_cast<const float4*>(row + at);
-  const float4* s = reinterpret_cast<const float4*>(row + rot / 2 + at);
-  const float4 x = __ldg(c), y = __ldg(c + 1), z = __ldg(s), w = __ldg(s + 1);
-  a.c[0] = x.x, a.c[1] = x.y, a.c[2] = x.z, a.c[3] = x.w, a.c[4] = y.x, a.c[5] = y.y, a.c[6] = y.z, a.c[7] = y.w;
-  a.s[0] = z.x, a.s[1] = z.y, a.s[2] = z.z, a.s[3] = z.w, a.s[4] = w.x, a.s[5] = w.y, a.s[6] = w.z, a.s[7] = w.w;
-}
-enum TurnAs { kExact, kPlain, kNear };
-template <TurnAs HOW>
-__device__ __forceinline__ void turn(float* x, const Angles& a, bool interleaved) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& u = interleaved ? x[2 * i] : x[i];
-    float& w = interleaved ? x[2 * i + 1] : x[8 + i];
-    const float p = u, q = w;
-    if (HOW == kExact) {
-      u = diff_of_products(p, a.c[i], q, a.s[i]);
-      w = diff_of_products(q, a.c[i], -p, a.s[i]);
-    } else if (HOW == kPlain) {
-      u = p * a.c[i] - q * a.s[i];
-      w = q * a.c[i] + p * a.s[i];
-    } else {  // an output of 16 bits: one rounding of a product's error is enough
-      const float m = __fmul_rn(q, a.s[i]), n = __fmul_rn(p, a.s[i]);
-      u = __fsub_rn(__fmaf_rn(p, a.c[i], -m), __fmaf_rn(q, a.s[i], -m));
-      w = __fadd_rn(__fmaf_rn(q, a.c[i], n), __fmaf_rn(p, a.s[i], -n));
-    }
-  }
-}
-
-// The query part: thread `at` turns the same channels of 4 heads of one token.
-template <bool INTERLEAVED, bool HALF>
-__device__ __forceinline__ void rotate_queries(const PagedAppendParams& p, int64_t at) {
-  constexpr bool half = HALF;
-  const int lanes = p.D / 16, P = p.c.P;
-  const int groups = (p.Hq + 3) / 4;
-  const int j = (int)(at % lanes);
-  const int64_t rest = at / lanes;
-  const int hg = (int)(rest % groups);
-  const int64_t t = rest / groups;
-  if (t >= p.b.n_new) return;
-  const Runs r = lane_runs(j, p.rot, INTERLEAVED);
-  const int heads = min(4, p.Hq - hg * 4);
-  Raw raw[4];  // under way before the token's sequence is known
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
-    if (h < heads) raw[h] = load_runs(p.q + t * p.q_stride + (int64_t)(hg * 4 + h) * p.D, r);
-  // the token's sequence: the last b with cu[b] <= t
-  int lo = 0, hi = p.b.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.b.cu[mid] <= t) lo = mid; else hi = mid;
-  }
-  bool bad;
-  const Seq s = read_seq(p.b, lo, P, &bad);
-  if (t < s.t0 || t >= s.t0 + s.n) return;  // a row behind the last sequence
-  Angles a;
-  if (r.angle >= 0) {
-    const int pos = s.len - s.n + (int)(t - s.t0);
-    if (pos < 0 || pos >= p.n_pos) raise(p.status, HYB_STATUS_BAD_LENGTH);
-    load_angles(a, p.rope + (int64_t)min(max(pos, 0), p.n_pos - 1) * p.rot, p.rot, r.angle);
-  }
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    if (h >= heads) break;
-    float x[16];
-    to_values(raw[h], half, x);
-    if (r.angle >= 0) turn<kNear>(x, a, INTERLEAVED);
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_out(x[2 * i], x[2 * i + 1], half);
-    uint16_t* row = p.q_out + t * p.qo_stride + (int64_t)(hg * 4 + h) * p.D;
-    *reinterpret_cast<uint4*>(row + r.c0) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(row + r.c1) = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
-template <bool INTERLEAVED, bool HALF>
-__global__ void __launch_bounds__(kRotateThreads, 4) paged_rotate_kernel(const PagedAppendParams p) {
-  rotate_queries<INTERLEAVED, HALF>(p, (int64_t)blockIdx.x * kRotateThreads + threadIdx.x);
-}
-
-template <bool INTERLEAVED, bool HALF, bool INT8>
-__global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendParams p) {
-  constexpr bool half = HALF;
-  const int lanes = p.D / 16;  // lanes of a row: 4 or 8
-  const int P = p.c.P;
-
-  if ((int64_t)blockIdx.x >= p.kv_blocks) {
-    rotate_queries<INTERLEAVED, HALF>(p, ((int64_t)blockIdx.x - p.kv_blocks) * blockDim.x + threadIdx.x);
-    return;
-  }
-
-  // The cache part: blocks ordered by sequence, page, KV head, keys / values.
-  uint32_t bi = blockIdx.x;
-  const bool values = bi & 1;
-  bi >>= 1;
-  const int h = (int)(bi % (uint32_t)p.c.Hkv);
-  bi /= (uint32_t)p.c.Hkv;
-  const int pi = (int)(bi % (uint32_t)p.pages_max);
-  const int b = (int)(bi / (uint32_t)p.pages_max);
-  bool bad;
-  const Seq s = read_seq(p.b, b, P, &bad);
-  if (bad && pi == 0 && h == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
-  const int start = s.len - s.n;  // position of the first new token
-  const int first = max(start, 0);
-  if (start < 0 && pi == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
-  const int pg = first / P + pi;  // page of the sequence
-  const int lo = max(pg * P, first), hi = (int)min((int64_t)(pg + 1) * P, (int64_t)s.len);
-  if (lo >= hi) return;
-  const int j = threadIdx.x % lanes, row0 = threadIdx.x / lanes, step = blockDim.x / lanes;
-  const Runs r = lane_runs(j, values ? 0 : p.rot, INTERLEAVED);
-  const uint16_t* in = values ? p.v : p.k;
-  const int64_t stride = values ? p.v_stride : p.k_stride;
-  Raw raw[kAppendRows];  // under way before the page is known
-#pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    const int pos = lo + row0 + i * step;
-    if (pos < hi) raw[i] = load_runs(in + (int64_t)(s.t0 + pos - start) * stride + (int64_t)h * p.D, r);
-  }
-  const int page = p.b.table[(int64_t)b * p.b.mp + pg];
-  if (page < 0 || page >= p.c.n_pages) {
-    if (threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_PAGE);
-    return;
-  }
-  float* scale_at = (values ? p.c.vs : p.c.ks) + (int64_t)page * p.c.Hkv + h;
-  uint8_t* codes = (values ? p.c.v : p.c.k) + ((int64_t)page * p.c.Hkv + h) * P * p.D;
-  const int older = lo - pg * P;  // tokens that the page held before
-  const float was = older > 0 ? *scale_at : 0.f;
-
-  float x[kAppendRows][16];
-  uint32_t top = 0;  // the largest magnitude's bits, which order like it; past those of FLT_MAX where one is not finite
-#pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    const int pos = lo + row0 + i * step;
-    if (pos >= hi) continue;
-    to_values(raw[i], half, x[i]);
-    if (r.angle >= 0) {
-      Angles a;
-      if (pos >= p.n_pos) raise(p.status, HYB_STATUS_BAD_LENGTH);
-      load_angles(a, p.rope + (int64_t)min(pos, p.n_pos - 1) * p.rot, p.rot, r.angle);
-      turn<kExact>(x[i], a, INTERLEAVED);
-    }
-#pragma unroll
-    for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(x[i][c]) & 0x7fffffffu);
-  }
-  __shared__ uint32_t part[2][16];
-  auto block_top = [&](uint32_t* shared) {
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = max(top, shared[w]);
-  };
-  block_top(part[0]);
-  if (top >= 0x7f800000u) {
-    // Some value is not finite.  Take the plain rotation where the exact one has no value, store NaN as 0, and leave
-    // what is not finite out of the scale.
-    bool odd = false;
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < kAppendRows; ++i) {
-      const int pos = lo + row0 + i * step;
-      if (pos >= hi) continue;
-      float y[16];
-      to_values(load_runs(in + (int64_t)(s.t0 + pos - start) * stride + (int64_t)h * p.D, r), half, y);
-      if (r.angle >= 0) {
-        Angles a;
-        load_angles(a, p.rope + (int64_t)min(pos, p.n_pos - 1) * p.rot, p.rot, r.angle);
-        turn<kPlain>(y, a, INTERLEAVED);
-      }
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        if (!isfinite(x[i][c])) x[i][c] = y[c];
-        odd |= !isfinite(x[i][c]);
-        if (isnan(x[i][c])) x[i][c] = 0.f;
-        if (!isinf(x[i][c])) top = max(top, __float_as_uint(x[i][c]) & 0x7fffffffu);
-      }
-    }
-    if (odd) raise(p.status, HYB_STATUS_NONFINITE);
-    block_top(part[1]);
-  }
-  const float amax = __uint_as_float(top);
-  const float need = scale_for<INT8>(amax);
-  // a scale only grows while the page holds tokens (a NaN left there is replaced)
-  const float now = older > 0 && was >= need ? was : need;
-  const float inv = __fdiv_rn(1.f, now);
-  if (older > 0 && now != was) {
-    const float ratio = __fmul_rn(was, inv);
-    const int words = older * p.D / 4;
-    for (int w = threadIdx.x; w < words; w += blockDim.x) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(codes) + w;
-      const uint32_t c = *at;
-      float y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = value_of<INT8>((c >> (8 * i)) & 0xffu);
-      *at = code4<INT8>(y, ratio);
-    }
-  }
-  if (threadIdx.x == 0 && !(older > 0 && now == was)) *scale_at = now;
-#pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    const int pos = lo + row0 + i * step;
-    if (pos >= hi) continue;
-    uint8_t* row = codes + (int64_t)(pos - pg * P) * p.D;
-    *reinterpret_cast<uint2*>(row + r.c0) = make_uint2(code4<INT8>(x[i], inv), code4<INT8>(x[i] + 4, inv));
-    *reinterpret_cast<uint2*>(row + r.c1) = make_uint2(code4<INT8>(x[i] + 8, inv), code4<INT8>(x[i] + 12, inv));
-  }
-}
-
-// ================================================================================================
-// Attention
-// ================================================================================================
-//
 // With codes c and scales: k_t = ks c_t, v_t = vs c_t (ks, vs of t's page).  A
 // row's logits in powers of two are z_t = (q . c_t) ks scale log2(e), its output
 // sum_t 2^(z_t - m) vs c_t / sum_t 2^(z_t - m) with the running maximum m.
@@ -413,62 +65,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four codes to two f16 pairs (bytes 0, 1 and bytes 2, 3), exactly.
-template <bool INT8>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (INT8) {
-    // 1024 + (c + 128) has the byte c + 128 as its low bits; c + 128 is c with the sign bit flipped
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __floats2half2_rn(1152.f, 1152.f);
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<uint32_t*>(&x);
-    hi = *reinterpret_cast<uint32_t*>(&y);
-  } else {
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Exponent field of the power of two at or above x (0 <= x <= 2^126, the scales'
-// range), at least 2^-126; infinity and NaN give 2^126, and the weights take them on.
-__device__ __forceinline__ uint32_t pow2_above(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return min(max((u >> 23) + ((u & 0x7fffffu) ? 1u : 0u), 1u), 253u);
-}
-__device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
-
-// Where the visible tokens of a row tile lie: sinks [0, sink), then [lo, hi)
-// from a multiple of 16; 32-token stages, the sinks' first.
-struct Span {
-  int sink, lo, hi, sink_stages, stages;
-};
-__device__ __forceinline__ Span make_span(int pos_min, int pos_max, int W, int S) {
-  Span s;
-  s.hi = pos_max + 1;
-  s.lo = W > 0 ? max(pos_min - W + 1, 0) & ~15 : 0;
-  s.sink = W > 0 ? min(S, s.lo) : 0;
-  s.sink_stages = (s.sink + kStageTokens - 1) / kStageTokens;
-  s.stages = s.sink_stages + (max(s.hi - s.lo, 0) + kStageTokens - 1) / kStageTokens;
-  return s;
-}
-__device__ __forceinline__ void stage_range(const Span& s, int st, int& base, int& end) {
-  if (st < s.sink_stages) {
-    base = st * kStageTokens;
-    end = min(base + kStageTokens, s.sink);
-  } else {
-    base = s.lo + (st - s.sink_stages) * kStageTokens;
-    end = min(base + kStageTokens, s.hi);
-  }
-}
-
 // Pages of a stage's two 16-token groups (-1: none, or out of range).
 struct StagePages {
   int p0, p1, o0, o1;  // pages, and the groups' first tokens within them
@@ -799,96 +395,6 @@ __device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, floa
 // 16 rows each) take its stages in turn and are joined at each unit's end.  A unit that
 // more than one CTA worked on is joined by paged_join_kernel.
 
-__device__ __forceinline__ Span seq_span(const PagedAttnParams& p, const Seq& s) {
-  if (s.n == 0) return Span{0, 0, 0, 0, 0};
-  return make_span(max(s.len - s.n, 0), s.len - 1, p.W, p.S);
-}
-
-// The line's geometry, in all lanes of a warp.  Stage counts fit 31 bits (the host
-// refuses more).
-struct Line {
-  uint32_t total;   // stages in all
-  uint32_t per;     // of each CTA: a multiple of its warps
-  uint32_t mine;    // lane's: stages of all units of sequence `lane`, and those before it
-  uint32_t before;
-};
-
-// Stages of all of a sequence's units.
-__device__ __forceinline__ uint32_t seq_stages(const PagedAttnParams& p, int b) {
-  bool bad;
-  const Seq s = read_seq(p.b, b, p.c.P, &bad);
-  return (uint32_t)seq_span(p, s).stages * (uint32_t)p.c.Hkv;
-}
-__device__ __forceinline__ uint32_t warp_sum(uint32_t x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ uint32_t warp_upto(uint32_t x) {  // inclusive prefix sum over the lanes
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-__device__ __forceinline__ Line make_line(const PagedAttnParams& p) {
-  const int lane = threadIdx.x & 31;
-  Line l;
-  l.mine = lane < p.b.B ? seq_stages(p, lane) : 0;
-  const uint32_t upto = warp_upto(l.mine);
-  l.before = upto - l.mine;
-  l.total = __shfl_sync(0xffffffffu, upto, 31);
-  if (p.b.B > 32) {
-    uint32_t sum = 0;
-    for (int b = 32 + lane; b < p.b.B; b += 32) sum += seq_stages(p, b);
-    l.total += warp_sum(sum);
-  }
-  const uint32_t n = (uint32_t)p.n_cta * kWarps;
-  l.per = ((l.total + n - 1) / n) * kWarps;
-  return l;
-}
-// The sequence that stage x < total lies in, and the stage at which its first unit begins.
-__device__ __forceinline__ int line_find(const PagedAttnParams& p, const Line& l, uint32_t x, uint32_t& begin) {
-  const int lane = threadIdx.x & 31;
-  uint32_t past = __ballot_sync(0xffffffffu, l.before + l.mine > x);
-  if (past) {
-    const int at = __ffs(past) - 1;
-    begin = __shfl_sync(0xffffffffu, l.before, at);
-    return at;
-  }
-  uint32_t before = __shfl_sync(0xffffffffu, l.before + l.mine, 31);
-  for (int b0 = 32; b0 < p.b.B; b0 += 32) {
-    const uint32_t mine = b0 + lane < p.b.B ? seq_stages(p, b0 + lane) : 0;
-    const uint32_t upto = before + warp_upto(mine);
-    past = __ballot_sync(0xffffffffu, upto > x);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      begin = __shfl_sync(0xffffffffu, upto - mine, at);
-      return b0 + at;
-    }
-    before = __shfl_sync(0xffffffffu, upto, 31);
-  }
-  begin = before;
-  return p.b.B - 1;
-}
-
-__device__ __forceinline__ void store_row(const PagedAttnParams& p, int64_t tok, int head, float lse2) {
-  if (p.lse != nullptr) p.lse[tok * p.Hq + head] = lse2;
-}
-
-constexpr float kLn2 = 0.6931471805599453f;
-// Natural logarithm of the sum whose weights are 2^(z - m + 15).
-__device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m - 15.f + log2f(l)) * kLn2; }
-
-__device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t tok, int hd, int D, int c, const float4& y,
-                                             float m, float l) {
-  *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + (int64_t)hd * D + 4 * c) =
-      make_uint2(pack_out(y.x, y.y, p.half), pack_out(y.z, y.w, p.half));
-  if (c == 0) store_row(p, tok, hd, lse_of(m, l));
-}
-
 template <int GW>
 __device__ __forceinline__ void team_sync() {
   if (GW == 1) {
@@ -912,17 +418,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
   uint8_t* ring = smem + team * kRing * kBytes;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
 
-  const Line line = make_line(p);
+  const Line line = make_line<kStageTokens>(p);
   const uint32_t first = min(line.per * blockIdx.x, line.total), last = min(first + line.per, line.total);
   uint32_t at = first;
   pdl_allow_dependents();  // the join may take its place; it waits for this grid's end
   while (at < last) {
     // the unit that stage `at` lies in, and the part of it that is this CTA's
     uint32_t begin;
-    const int b = line_find(p, line, at, begin);
+    const int b = line_find<kStageTokens>(p, line, at, begin);
     bool bad;
     const Seq seq = read_seq(p.b, b, p.c.P, &bad);
-    const Span span = seq_span(p, seq);
+    const Span<kStageTokens> span = seq_span<kStageTokens>(p, seq);
     const int h = (int)((at - begin) / (uint32_t)span.stages);
     const uint32_t ubegin = begin + (uint32_t)h * span.stages;
     const int s0 = (int)(at - ubegin), s1 = (int)min((uint32_t)span.stages, last - ubegin);
@@ -1083,7 +589,7 @@ __device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& s
 
 // Joins the parts of units that more than one CTA worked on, and writes the rows
 // of units with no visible token.  One CTA a (unit, row).
-template <int D>
+template <int D, int T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnParams p, int tile_rows) {
   const int unit = blockIdx.x, row = blockIdx.y;
   const int b = unit / p.c.Hkv, h = unit % p.c.Hkv;
@@ -1095,18 +601,18 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   }
   const int64_t tok = seq.t0 + row / p.G;
   const int hd = h * p.G + row % p.G;
-  const int stages = seq_span(p, seq).stages;
+  const int stages = seq_span<T>(p, seq).stages;
   if (stages == 0) {
     pdl_wait_primary();
     if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
     return;
   }
   // the line up to this sequence
-  const Line line = make_line(p);
+  const Line line = make_line<T>(p);
   uint32_t begin = __shfl_sync(0xffffffffu, line.before, b & 31);
   if (b >= 32) {
     uint32_t sum = 0;
-    for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_stages(p, i);
+    for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_stages<T>(p, i);
     begin = warp_sum(sum);
   }
   begin += (uint32_t)h * stages;
@@ -1148,7 +654,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
   const int rows = seq.n * p.G, row0 = tile * kWideRows, pos0 = seq.len - seq.n;
   if (row0 >= rows) return;
   const int pos_min = pos0 + row0 / p.G, pos_max = pos0 + (min(rows, row0 + kWideRows) - 1) / p.G;
-  const Span span = pos_max >= 0 ? make_span(max(pos_min, 0), pos_max, p.W, p.S) : Span{0, 0, 0, 0, 0};
+  const Span<kStageTokens> span = pos_max >= 0 ? make_span<kStageTokens>(max(pos_min, 0), pos_max, p.W, p.S) : Span<kStageTokens>{0, 0, 0, 0, 0};
   const int s0 = (int)((int64_t)span.stages * split / p.n_splits);
   const int s1 = (int)((int64_t)span.stages * (split + 1) / p.n_splits);
   const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
@@ -1233,26 +739,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_rows_kernel(const Pag
   if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, y, m, l);
 }
 
-// ---- launches -----------------------------------------------------------------------------------------
-template <class... A>
-cudaError_t launch(void (*f)(A...), dim3 grid, dim3 block, size_t smem, bool chained, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid;
-  c.blockDim = block;
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = attr;
-  c.numAttrs = chained ? 1 : 0;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaLaunchKernelEx(&c, f, args...);
-}
-
 template <int D, bool INT8, int NT, int GW, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
   constexpr int kRows = 8 * NT * GW;
@@ -1261,7 +747,7 @@ cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
   cudaError_t e = launch(paged_narrow_kernel<D, INT8, NT, GW, FINE>, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess) return e;
   const int n = p.b.max_new * p.G < kRows ? p.b.max_new * p.G : kRows;
-  return launch(paged_join_kernel<D>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, kRows);
+  return launch(paged_join_kernel<D, kStageTokens>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, kRows);
 }
 template <int D, bool INT8, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, int rows, cudaStream_t s) {
@@ -1281,32 +767,20 @@ cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
                          dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(kJoinThreads), 0, true, s, p);
+  return launch_paged_join_rows(p, D, s);
 }
 
 }  // namespace
 
-namespace {
-template <bool INTERLEAVED, bool HALF>
-cudaError_t append(const PagedAppendParams& p, cudaStream_t s) {
-  const int lanes = p.D / 16;
-  const int threads = (p.c.P * lanes / kAppendRows + 31) / 32 * 32;
-  const int64_t q_threads = p.q != nullptr ? (int64_t)p.b.n_new * ((p.Hq + 3) / 4) * lanes : 0;
-  // Many queries go in a launch of their own, whose fewer registers let more of them be under way (32K tokens of 32
-  // heads: 83 us, the copy bandwidth); for few, one launch less counts more.
-  const bool apart = q_threads >= kRotateApart;
-  const int64_t blocks = p.kv_blocks + (apart ? 0 : (q_threads + threads - 1) / threads);
-  const cudaError_t e = launch(p.int8 ? paged_append_kernel<INTERLEAVED, HALF, true> : paged_append_kernel<INTERLEAVED, HALF, false>,
-                               dim3((unsigned)blocks), dim3(threads), 0, false, s, p);
-  if (!apart || e != cudaSuccess) return e;
-  return launch(paged_rotate_kernel<INTERLEAVED, HALF>, dim3((unsigned)((q_threads + kRotateThreads - 1) / kRotateThreads)),
-                dim3(kRotateThreads), 0, false, s, p);
+cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStream_t s) {
+  const int n = p.b.max_new * p.G < rows ? p.b.max_new * p.G : rows;
+  const dim3 grid(p.b.B * p.c.Hkv, n), block(kJoinThreads);
+  if (D == 128) return launch(paged_join_kernel<128, 128>, grid, block, 0, true, s, p, rows);
+  return launch(paged_join_kernel<64, 128>, grid, block, 0, true, s, p, rows);
 }
-}  // namespace
-
-cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
-  if (p.half) return p.interleaved ? append<true, true>(p, s) : append<false, true>(p, s);
-  return p.interleaved ? append<true, false>(p, s) : append<false, false>(p, s);
+cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s) {
+  const dim3 grid(p.Hq, p.b.max_new, p.b.B), block(kJoinThreads);
+  return D == 128 ? launch(paged_join_rows_kernel<128>, grid, block, 0, true, s, p) : launch(paged_join_rows_kernel<64>, grid, block, 0, true, s, p);
 }
 
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int rows, cudaStream_t s) {

@@ -49,8 +49,9 @@ struct PagedAttnParams {
   int64_t q_stride, out_stride;
   int32_t Hq, G, half, W, S;
   float scale;       // times log2(e)
-  int32_t n_cta;     // CTAs that share the stages of all units (narrow form)
-  int32_t n_splits;  // parts of each row tile's stages (wide form)
+  int32_t n_cta;     // CTAs that share the line of all units' stages
+  int32_t quantum;   // stages that a CTA's part is a multiple of
+  int32_t n_splits;  // parts of each row tile's stages (wide forms)
   float* ws;         // partial results
   uint32_t* status;
 };
@@ -60,9 +61,17 @@ struct PagedAttnParams {
 constexpr int kNarrowRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kCtasPerSm = 3;
+// Rows of a CTA of the form on tcgen05.
+constexpr int kMmaRows = 128;
+constexpr int kMmaCtasPerSm = 2;
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int rows, cudaStream_t s);
+cudaError_t launch_paged_mma(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
+
+// Joins of the parts that several CTAs left: of the line of 128-token tiles with `rows` rows a unit; of n_splits parts.
+cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStream_t s);
+cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s);
 
 }  // namespace hyb

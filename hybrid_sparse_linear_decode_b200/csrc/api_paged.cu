@@ -79,7 +79,9 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   int64_t len = std::min<int64_t>(b->max_len, (int64_t)b->table_stride * c->page_size);
   if (window > 0) len = std::min<int64_t>(len, (int64_t)window + sink + b->max_new + 64);
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
-  const bool mma = rows > kNarrowMost && type == HYB_TYPE_BF16;
+  // the tcgen05 form places codes in 16-byte pieces of 32 bits (64 GB of keys, and of values)
+  const bool fits = (int64_t)c->n_pages * c->n_kv_heads * c->page_size * (c->head_dim / 16) < 0xffffffffll;
+  const bool mma = rows > kNarrowMost && type == HYB_TYPE_BF16 && fits;
   p.form = mma ? Plan::kMma : rows <= kNarrowRows ? Plan::kNarrow : Plan::kWide;
   const int tile = mma ? kMmaRows : kWideRows;
   if (p.form == Plan::kNarrow || (mma && rows <= tile)) {

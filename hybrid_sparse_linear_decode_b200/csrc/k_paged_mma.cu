@@ -7,9 +7,8 @@
 //     over the columns of S; one of their threads issues S = Q C_k^T and O += P C_v (accumulators S [128 x 128] and
 //     O [128 x D] in tensor memory).
 // Within a CTA the products and the softmax of a tile follow one another; two CTAs share an SM, and the one's softmax
-// runs beside the other's products.  A row's maximum is followed only when a tile passes it by more than 2^8: the
-// weights of a tile are formed from the maximum so far, held in registers, and formed again in the rare case, in which
-// O is rescaled too.  They are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest.
+// runs beside the other's products.  A row's maximum is followed only when a tile passes it by more than 2^8, so O is
+// rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest.
 #include "k_paged.cuh"
 
 namespace hyb {
@@ -82,12 +81,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -215,7 +214,6 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
   using Geo = MmaGeo<D>;
   constexpr int kN = Pieces<D>::kN, kPerRow = D / 16, kStep = 128 / kPerRow;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
-  const int64_t head_bytes = (int64_t)p.c.P * D;
   Work w;
   Piece x;
   start_work(p, w);
@@ -224,26 +222,33 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
     if (x.s0 >= x.s1) continue;
     const int32_t* table = p.b.table + (int64_t)x.b * p.b.mp;
     Pieces<D> c;
-    int page[kN], gpage = -1;  // pages of the tile to be loaded next, and of this thread's group's scales
-    int base, end;
+    // where this thread's pieces of the tile to be loaded next begin, in pieces (kNone: no token there), and the page of
+    // this thread's group's scales
+    constexpr uint32_t kNone = 0xffffffffu;
+    uint32_t from[kN];
+    int entry[kN], gpage = -1, base, end;
     float ks, vs;
     int live;
-    auto pages = [&](int s) {
+    auto entries = [&](int s) {
       stage_range(x.span, s, base, end);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) page[i] = entry_of(p, table, (base + tid / kPerRow + i * kStep) & ~15, end, magic);
+      for (int i = 0; i < kN; ++i) entry[i] = entry_of(p, table, (base + tid / kPerRow + i * kStep) & ~15, end, magic);
       if (tid < kGroups) gpage = entry_of(p, table, base + 16 * tid, end, magic);
     };
-    auto load = [&](const uint8_t* from, uint4 (&to)[kN]) {
+    auto places = [&]() {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int tok = base + tid / kPerRow + i * kStep;
         const int in = tok - (p.c.P == 16 ? tok >> 4 : (int)__umulhi((uint32_t)tok >> 4, magic)) * p.c.P;
-        to[i] = (uint32_t)page[i] < (uint32_t)p.c.n_pages && tok < end
-                    ? __ldg(reinterpret_cast<const uint4*>(from + ((int64_t)page[i] * p.c.Hkv + x.h) * head_bytes + (int64_t)in * D +
-                                                           (tid % kPerRow) * 16))
-                    : make_uint4(0, 0, 0, 0);
+        from[i] = (uint32_t)entry[i] < (uint32_t)p.c.n_pages && tok < end
+                      ? (((uint32_t)entry[i] * p.c.Hkv + x.h) * p.c.P + in) * kPerRow + tid % kPerRow
+                      : kNone;
       }
+    };
+    auto load = [&](const uint8_t* codes, uint4 (&to)[kN]) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        to[i] = from[i] != kNone ? __ldg(reinterpret_cast<const uint4*>(codes) + from[i]) : make_uint4(0, 0, 0, 0);
     };
     auto load_scales = [&]() {
       ks = vs = 0.f;
@@ -256,13 +261,14 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
         live = min(max(end - base - 16 * tid, 0), 16);
       }
     };
-    pages(x.s0);
+    entries(x.s0);
+    places();
     load(p.c.k, c.k);
     load_scales();
     load(p.c.v, c.v);
     for (int s = x.s0; s < x.s1; ++s, ++t) {
       const bool more = s + 1 < x.s1;
-      if (more) pages(s + 1);
+      if (more) entries(s + 1);
       if (t > 0 && !warp_wait(p, bars + kKFree, (t - 1) & 1)) return;
       store_pieces<D, INT8>(smem + Geo::kK, c.k, tid);
       if (tid < kGroups) {
@@ -272,7 +278,7 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
       }
       fence_smem();
       mbar_arrive(bars + kKFull);
-      if (more) load(p.c.k, c.k), load_scales();
+      if (more) places(), load(p.c.k, c.k), load_scales();
       if (t > 0 && !warp_wait(p, bars + kVFree, (t - 1) & 1)) return;
       store_pieces<D, INT8>(smem + Geo::kV, c.v, tid);
       fence_smem();
@@ -309,6 +315,29 @@ __device__ __forceinline__ bool issue_outputs(uint32_t sm, uint64_t* bars, uint3
 }
 
 // ---- the softmax warps -------------------------------------------------------------------------------------------
+// Two 32-bit values at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 w, x, y, z; "
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
@@ -380,53 +409,38 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
 #pragma unroll
           for (int i = 0; i < kGroups; ++i) now = max(now, pow2_above(sc[kGroups + i]));
           const float down = pow2_of(254u - now);
-          uint32_t w[kTile / 2];
-          float sum, top;
-          // the weights of the tile for the maximum `from`, and the tile's own
-          auto weights = [&](float from) {
-            const float shift = from == -INFINITY ? 0.f : from - kBase;
-            sum = 0.f;
-            top = -INFINITY;
-            uint32_t r[2][16];
-            tmem_load16(mine, r[0]);
-#pragma unroll
-            for (int c = 0; c < kGroups; ++c) {
-              tmem_wait_load();
-              if (c + 1 < kGroups) tmem_load16(mine + 16 * (c + 1), r[(c + 1) & 1]);
-              const uint32_t(&z)[16] = r[c & 1];
-              const float f = sc[c] * rf, v = sc[kGroups + c] * down;
-              // which of the 16 tokens the row sees
-              const int at = base + 16 * c;
-              uint32_t see = low_bits(pos - at + 1) & low_bits(live[c]);
-              if (p.W > 0) see &= ~low_bits(pos - p.W + 1 - at) | low_bits(p.S - at);
-              float a[16], u[2] = {-INFINITY, -INFINITY}, add[2] = {0.f, 0.f};
-              if (__all_sync(0xffffffffu, see == 0xffffu)) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  u[i & 1] = fmaxf(u[i & 1], __uint_as_float(z[i]));
-                  a[i] = exp2_fast(__uint_as_float(z[i]) * f - shift);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const bool in = (see >> i) & 1u;
-                  u[i & 1] = fmaxf(u[i & 1], in ? __uint_as_float(z[i]) : -INFINITY);
-                  a[i] = in ? exp2_fast(__uint_as_float(z[i]) * f - shift) : 0.f;
-                }
-              }
-              // scales are not negative, so the largest product gives the largest logit
-              const float most = fmaxf(u[0], u[1]);
-              top = fmaxf(top, most == -INFINITY ? -INFINITY : most * f);
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                add[0] += a[i];
-                add[1] += a[i + 1];
-                w[8 * c + i / 2] = pack_half(a[i] * v, a[i + 1] * v);
-              }
-              sum += add[0] + add[1];
-            }
+          // which of 32 tokens the row sees
+          auto seen = [&](int c) {
+            const int at = base + 32 * c;
+            uint32_t see = low_bits(pos - at + 1) & (low_bits(live[2 * c]) | (low_bits(live[2 * c + 1]) << 16));
+            if (p.W > 0) see &= ~low_bits(pos - p.W + 1 - at) | low_bits(p.S - at);
+            return see;
           };
-          weights(m);
+          // The tile's maximum.  Loops are not unrolled: a warp alone on its scheduler runs straight code at the rate
+          // at which it is fetched.
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_load(mine + 32 * c, r);
+            const uint32_t see = seen(c);
+            const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+            tmem_wait_load();
+            float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (!all) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = (see >> i) & 1u ? r[i] : 0xff800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                u[2 * (i / 16) + e] = fmaxf(u[2 * (i / 16) + e], fmaxf(__uint_as_float(r[i + 2 * e]), __uint_as_float(r[i + 2 * e + 1])));
+            // scales are not negative, so the largest product gives the largest logit
+            const float u0 = fmaxf(u[0], u[1]), u1 = fmaxf(u[2], u[3]);
+            top = fmaxf(top, u0 == -INFINITY ? -INFINITY : u0 * (sc[2 * c] * rf));
+            top = fmaxf(top, u1 == -INFINITY ? -INFINITY : u1 * (sc[2 * c + 1] * rf));
+          }
           const bool grown = m == -INFINITY ? top > m : top > m + kGrowth;
           if (__any_sync(0xffffffffu, grown || now != ref)) {
             const float mn = grown ? top : m;
@@ -446,11 +460,35 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
             }
             m = mn;
             ref = now;
-            weights(m);
           }
-          l += sum;
-          tmem_store32(mine, *reinterpret_cast<const uint32_t(*)[32]>(w));
-          tmem_store32(mine + 32, *reinterpret_cast<const uint32_t(*)[32]>(w + 32));
+          const float shift = m == -INFINITY ? 0.f : kBase - m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32], w[16];
+            tmem_load(mine + 32 * c, r);
+            const uint32_t see = seen(c);
+            const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+            const float f0 = sc[2 * c] * rf, f1 = sc[2 * c + 1] * rf, v0 = sc[kGroups + 2 * c] * down, v1 = sc[kGroups + 2 * c + 1] * down;
+            float2 add = make_float2(0.f, 0.f);
+            const float2 nn = make_float2(shift, shift);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 ff = i < 16 ? make_float2(f0, f0) : make_float2(f1, f1);
+              const float2 vv = i < 16 ? make_float2(v0, v0) : make_float2(v1, v1);
+              float2 a = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ff, nn);
+              a.x = exp2_fast(a.x), a.y = exp2_fast(a.y);
+              if (!all) {
+                if (!((see >> i) & 1u)) a.x = 0.f;
+                if (!((see >> (i + 1)) & 1u)) a.y = 0.f;
+              }
+              add = add2(add, a);
+              const float2 b = mul2(a, vv);
+              w[i / 2] = pack_half(b.x, b.y);
+            }
+            l += add.x + add.y;
+            tmem_store16(mine + 16 * c, w);  // over columns of S that every lane of this warp has read
+          }
           tmem_wait_store();
         }
         fence_before();

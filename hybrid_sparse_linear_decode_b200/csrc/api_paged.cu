@@ -85,7 +85,7 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   p.form = mma ? Plan::kMma : rows <= kNarrowRows ? Plan::kNarrow : Plan::kWide;
   const int tile = mma ? kMmaRows : kWideRows;
   if (p.form == Plan::kNarrow || (mma && rows <= tile)) {
-    const int64_t stage = mma ? kMmaTokens : 32, warps = mma ? 1 : 4;
+    const int64_t stage = mma ? 128 : 32, warps = mma ? 1 : 4;
     const int64_t stages = std::max<int64_t>(1, (len + stage - 1) / stage);
     p.rows = mma ? tile : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * (mma ? kMmaCtasPerSm : kCtasPerSm), (units * stages + warps - 1) / warps));

@@ -775,8 +775,8 @@ cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
 cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStream_t s) {
   const int n = p.b.max_new * p.G < rows ? p.b.max_new * p.G : rows;
   const dim3 grid(p.b.B * p.c.Hkv, n), block(kJoinThreads);
-  if (D == 128) return launch(paged_join_kernel<128, kMmaTokens>, grid, block, 0, true, s, p, rows);
-  return launch(paged_join_kernel<64, kMmaTokens>, grid, block, 0, true, s, p, rows);
+  if (D == 128) return launch(paged_join_kernel<128, 128>, grid, block, 0, true, s, p, rows);
+  return launch(paged_join_kernel<64, 128>, grid, block, 0, true, s, p, rows);
 }
 cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s) {
   const dim3 grid(p.Hq, p.b.max_new, p.b.B), block(kJoinThreads);

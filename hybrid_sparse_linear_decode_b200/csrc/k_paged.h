@@ -61,9 +61,8 @@ struct PagedAttnParams {
 constexpr int kNarrowRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kCtasPerSm = 3;
-// Rows of a CTA of the form on tcgen05, and tokens of a tile.
+// Rows of a CTA of the form on tcgen05.
 constexpr int kMmaRows = 128;
-constexpr int kMmaTokens = 64;
 constexpr int kMmaCtasPerSm = 2;
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
@@ -71,7 +70,7 @@ cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int r
 cudaError_t launch_paged_mma(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 
-// Joins of the parts that several CTAs left: of the line of kMmaTokens tiles with `rows` rows a unit; of n_splits parts.
+// Joins of the parts that several CTAs left: of the line of 128-token tiles with `rows` rows a unit; of n_splits parts.
 cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStream_t s);
 cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s);
 

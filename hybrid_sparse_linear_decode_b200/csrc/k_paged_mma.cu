@@ -1,39 +1,34 @@
 // Attention over the paged 8-bit cache for many query rows, on the tensor cores' own memory (tcgen05).
 //
-// A CTA takes 128 rows and passes the tokens they can see 64 at a time:
-//   four converting warps turn the tile's codes into f16 in shared memory, two tiles ahead (the next tile's codes are on
-//     their way in registers meanwhile), and one of their threads issues S = Q C_k^T;
-//   four softmax warps, a thread a row, read S, keep the running maximum and sum, and write the weights P as f16 over
-//     the columns of S; one of their threads issues O += P C_v.
-// The accumulators are in tensor memory: two of S [128 x 64], which take turns, so that a tile's logits are formed
-// during the softmax of the one before, and O [128 x D].  Two CTAs share an SM.  A row's maximum is followed only when
-// a tile passes it by more than 2^8, so O is rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with
-// full 11 bits down to 2^-21 of the largest.
+// A CTA takes 128 rows and passes the tokens they can see 128 at a time:
+//   four converting warps turn the tile's codes into f16 in shared memory (the next tile's codes are on their way in
+//     registers meanwhile);
+//   four softmax warps, a thread a row, read S, keep the running maximum and sum, and write the weights P as f16
+//     over the columns of S; one of their threads issues S = Q C_k^T and O += P C_v (accumulators S [128 x 128] and
+//     O [128 x D] in tensor memory).
+// Within a CTA the products and the softmax of a tile follow one another; two CTAs share an SM, and the one's softmax
+// runs beside the other's products.  A row's maximum is followed only when a tile passes it by more than 2^8, so O is
+// rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest.
 #include "k_paged.cuh"
 
 namespace hyb {
 namespace {
 
-constexpr int kTile = kMmaRows;     // rows
-constexpr int kTok = kMmaTokens;    // tokens
-constexpr int kGroups = kTok / 16;
+constexpr int kTile = 128;  // rows, and tokens
+constexpr int kGroups = kTile / 16;
 constexpr int kThreads = 256;
 constexpr float kGrowth = 8.f, kBase = 7.f;
 constexpr uint64_t kLimitNs = 1000000000ull;
 
 template <int D>
 struct MmaGeo {
-  // Q; two tiles each of keys and values; their scales and live tokens by 16-token groups; barriers; the tensor
-  // memory's address.  The tiles begin at multiples of 1024 bytes.
-  static constexpr int kCodes = kTok * D * 2;
-  static constexpr int kQ = 0, kK = kQ + kTile * D * 2, kV = kK + 2 * kCodes, kScales = kV + 2 * kCodes;
+  static constexpr int kQ = 0, kK = kQ + kTile * D * 2, kV = kK + kTile * D * 2, kScales = kV + kTile * D * 2;
+  // two tiles' scales and live tokens of each 16-token group; barriers; the tensor memory's address
   static constexpr int kLive = kScales + 2 * 2 * kGroups * 4, kBars = kLive + 2 * kGroups * 4, kTmem = kBars + 8 * 8,
-                       kTotal = kTmem + 16 + 1024;
-  static constexpr int kSubQ = kTile * 128, kSubTile = kTok * 128;  // 64 channels of all rows
+                       kTotal = kTmem + 16 + 1024;  // 1024: the tiles begin at a multiple of it
+  static constexpr int kSubTile = kTile * 128;      // 64 channels of all rows
 };
-// barriers, those of tiles in pairs; and the columns of O
-enum { kSFull, kVFull = 2, kVFree = 4, kQFull = 6, kOFull };
-constexpr int kO = 2 * kTok;
+enum { kKFull, kKFree, kVFull, kVFree, kSFull, kOFull };
 
 // ---- tcgen05 -------------------------------------------------------------------------------------------
 // Shared-memory matrix with rows of 64 f16 (128 bytes) in groups of 8 rows, pieces of 16 bytes moved within a row by
@@ -76,12 +71,15 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -116,7 +114,7 @@ __device__ __forceinline__ bool warp_wait(const PagedAttnParams& p, uint64_t* ba
 // line of all units' tiles, where every sequence has at most 128 rows a KV head; as many pieces as units in it.
 struct Piece {
   Seq seq;
-  Span<kTok> span;
+  Span<kTile> span;
   int b, h, row0, rows, s0, s1;
   int64_t slot;   // line: where a part's result goes
   bool complete;  // the piece is all of its row tile's tiles
@@ -129,7 +127,7 @@ struct Work {
 __device__ __forceinline__ void start_work(const PagedAttnParams& p, Work& w) {
   w.done = false;
   if (p.n_cta > 0) {
-    w.line = make_line<kTok>(p);
+    w.line = make_line<kTile>(p);
     w.first = min(w.line.per * blockIdx.x, w.line.total);
     w.last = min(w.first + w.line.per, w.line.total);
     w.at = w.first;
@@ -141,9 +139,9 @@ __device__ __forceinline__ bool next_piece(const PagedAttnParams& p, Work& w, Pi
   if (p.n_cta > 0) {
     if (w.at >= w.last) return false;
     uint32_t begin;
-    x.b = line_find<kTok>(p, w.line, w.at, begin);
+    x.b = line_find<kTile>(p, w.line, w.at, begin);
     x.seq = read_seq(p.b, x.b, p.c.P, &bad);
-    x.span = seq_span<kTok>(p, x.seq);
+    x.span = seq_span<kTile>(p, x.seq);
     x.h = (int)((w.at - begin) / (uint32_t)x.span.stages);
     const uint32_t ubegin = begin + (uint32_t)x.h * x.span.stages;
     x.s0 = (int)(w.at - ubegin);
@@ -164,7 +162,7 @@ __device__ __forceinline__ bool next_piece(const PagedAttnParams& p, Work& w, Pi
     if (x.row0 >= x.rows) return false;
     const int pos0 = x.seq.len - x.seq.n;
     const int lo = pos0 + x.row0 / p.G, hi = pos0 + (min(x.rows, x.row0 + kTile) - 1) / p.G;
-    x.span = hi >= 0 ? make_span<kTok>(max(lo, 0), hi, p.W, p.S) : Span<kTok>{0, 0, 0, 0, 0};
+    x.span = hi >= 0 ? make_span<kTile>(max(lo, 0), hi, p.W, p.S) : Span<kTile>{0, 0, 0, 0, 0};
     x.s0 = (int)((int64_t)x.span.stages * split / p.n_splits);
     x.s1 = (int)((int64_t)x.span.stages * (split + 1) / p.n_splits);
     x.complete = p.n_splits == 1;
@@ -174,34 +172,10 @@ __device__ __forceinline__ bool next_piece(const PagedAttnParams& p, Work& w, Pi
   return true;
 }
 
-// ---- the products (one thread) ----------------------------------------------------------------------------------
-template <int D>
-__device__ __forceinline__ void issue_logits(uint32_t sm, uint64_t* bars, uint32_t tmem, uint32_t two) {
-  using Geo = MmaGeo<D>;
-  const uint32_t keys = sm + Geo::kK + two * Geo::kCodes;
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k)
-    mma_smem(tmem + two * kTok, matrix_at(sm + Geo::kQ + (k / 4) * Geo::kSubQ + (k % 4) * 32, 16),
-             matrix_at(keys + (k / 4) * Geo::kSubTile + (k % 4) * 32, 16), product_of(kTok, false), k > 0);
-  commit_to(bars + kSFull + two);
-  mbar_arrive(bars + kSFull + two);  // with the products: what the converting warps wrote beside the codes
-}
-template <int D>
-__device__ __forceinline__ void issue_outputs(uint32_t sm, uint64_t* bars, uint32_t tmem, uint32_t two, bool first) {
-  using Geo = MmaGeo<D>;
-  const uint32_t values = sm + Geo::kV + two * Geo::kCodes;
-#pragma unroll
-  for (int k = 0; k < kTok / 16; ++k)
-    mma_tmem(tmem + kO, tmem + two * kTok + 8 * k, matrix_at(values + k * 16 * 128, Geo::kSubTile), product_of(D, true), !first || k > 0);
-  commit_to(bars + kVFree + two);
-}
-__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void codes_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
 // ---- the converting warps -----------------------------------------------------------------------------------
 template <int D>
 struct Pieces {
-  static constexpr int kN = kTok * D / 16 / 128;  // 16-code pieces of a thread, of keys and of values
+  static constexpr int kN = kTile * D / 16 / 128;  // 16-code pieces of a thread, of keys and of values
   uint4 k[kN], v[kN];
 };
 // The table's entry for the group of 16 tokens that begins at tok, -1 past the end.
@@ -236,16 +210,14 @@ __device__ __forceinline__ void store_pieces(uint8_t* tile, const uint4 (&c)[Pie
 }
 
 template <int D, bool INT8>
-__device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* bars, uint32_t tmem, int tid) {
+__device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* bars, int tid) {
   using Geo = MmaGeo<D>;
-  const uint32_t sm = smem_u32(smem);
   constexpr int kN = Pieces<D>::kN, kPerRow = D / 16, kStep = 128 / kPerRow;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
   Work w;
   Piece x;
   start_work(p, w);
-  uint32_t t = 0, pieces = 0;  // so far
-  bool alive = true, ok = true;  // after a wait that ran out the warps keep the barriers' count, and wait for nothing more
+  uint32_t t = 0;  // tiles so far
   while (next_piece(p, w, x)) {
     if (x.s0 >= x.s1) continue;
     const int32_t* table = p.b.table + (int64_t)x.b * p.b.mp;
@@ -296,40 +268,50 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
     load(p.c.v, c.v);
     for (int s = x.s0; s < x.s1; ++s, ++t) {
       const bool more = s + 1 < x.s1;
-      const uint32_t two = t & 1, turn = (t >> 1) & 1;  // the tile's buffers, and their barriers' parity
       if (more) entries(s + 1);
-      // the logits two tiles ago are done with the keys' buffer
-      if (t >= 2) alive = alive && warp_wait(p, bars + kSFull + two, turn ^ 1);
-      store_pieces<D, INT8>(smem + Geo::kK + two * Geo::kCodes, c.k, tid);
-      if (more) places(), load(p.c.k, c.k);
-      // the outputs two tiles ago are done with the values' buffer, the weights in this tile's columns and the scales
-      if (t >= 2) alive = alive && warp_wait(p, bars + kVFree + two, turn ^ 1);
+      if (t > 0 && !warp_wait(p, bars + kKFree, (t - 1) & 1)) return;
+      store_pieces<D, INT8>(smem + Geo::kK, c.k, tid);
       if (tid < kGroups) {
-        float* sc = reinterpret_cast<float*>(smem + Geo::kScales) + two * 2 * kGroups;
+        float* sc = reinterpret_cast<float*>(smem + Geo::kScales) + (t & 1) * 2 * kGroups;
         sc[tid] = ks, sc[kGroups + tid] = vs;
-        reinterpret_cast<int*>(smem + Geo::kLive)[two * kGroups + tid] = live;
+        reinterpret_cast<int*>(smem + Geo::kLive)[(t & 1) * kGroups + tid] = live;
       }
-      if (more) load_scales();
       fence_smem();
-      fence_before();
-      codes_sync();  // all of the keys are there
-      if (tid == 0 && ok) {
-        fence_after();
-        ok = alive && (s > x.s0 || wait_for(bars + kQFull, pieces & 1));
-        if (ok) {
-          issue_logits<D>(sm, bars, tmem, two);
-        } else {
-          raise(p.status, HYB_STATUS_TIMEOUT);
-        }
-      }
-      __syncwarp();
-      store_pieces<D, INT8>(smem + Geo::kV + two * Geo::kCodes, c.v, tid);
+      mbar_arrive(bars + kKFull);
+      if (more) places(), load(p.c.k, c.k), load_scales();
+      if (t > 0 && !warp_wait(p, bars + kVFree, (t - 1) & 1)) return;
+      store_pieces<D, INT8>(smem + Geo::kV, c.v, tid);
       fence_smem();
-      mbar_arrive(bars + kVFull + two);
+      mbar_arrive(bars + kVFull);
       if (more) load(p.c.v, c.v);
     }
-    ++pieces;
   }
+}
+
+// ---- the products (one thread) ----------------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ bool issue_logits(uint32_t sm, uint64_t* bars, uint32_t tmem, uint32_t t) {
+  using Geo = MmaGeo<D>;
+  if (!wait_for(bars + kKFull, t & 1)) return false;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t off = (k / 4) * Geo::kSubTile + (k % 4) * 32;
+    mma_smem(tmem, matrix_at(sm + Geo::kQ + off, 16), matrix_at(sm + Geo::kK + off, 16), product_of(kTile, false), k > 0);
+  }
+  commit_to(bars + kKFree);
+  commit_to(bars + kSFull);
+  mbar_arrive(bars + kSFull);  // with the products: what the converting warps wrote beside the codes
+  return true;
+}
+template <int D>
+__device__ __forceinline__ bool issue_outputs(uint32_t sm, uint64_t* bars, uint32_t tmem, uint32_t t, bool first) {
+  using Geo = MmaGeo<D>;
+  if (!wait_for(bars + kVFull, t & 1)) return false;
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    mma_tmem(tmem + kTile, tmem + 8 * k, matrix_at(sm + Geo::kV + k * 16 * 128, Geo::kSubTile), product_of(D, true), !first || k > 0);
+  commit_to(bars + kVFree);
+  return true;
 }
 
 // ---- the softmax warps -------------------------------------------------------------------------------------------
@@ -356,6 +338,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
 template <int D>
@@ -401,116 +384,125 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
           uint32_t y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[k] = pack_half(in_lo(u[k], half) * inv, in_hi(u[k], half) * inv);
-          *reinterpret_cast<uint4*>(smem + Geo::kQ + (i / 8) * Geo::kSubQ + tid * 128 + (((i % 8) ^ (tid & 7)) * 16)) =
+          *reinterpret_cast<uint4*>(smem + Geo::kQ + (i / 8) * Geo::kSubTile + tid * 128 + (((i % 8) ^ (tid & 7)) * 16)) =
               make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
-      // Q is there, and O of the piece before is read
+      // Q is there, and O and S of the piece before are read
       fence_smem();
       fence_before();
-      mbar_arrive(bars + kQFull);
+      rows_sync();
+      if (tid == 0 && ok) {
+        fence_after();
+        ok = issue_logits<D>(sm, bars, tmem, t);
+        if (!ok) raise(p.status, HYB_STATUS_TIMEOUT);
+      }
       for (int s = x.s0; s < x.s1; ++s, ++t) {
         int base, end;
         stage_range(x.span, s, base, end);
-        const uint32_t two = t & 1, turn = (t >> 1) & 1;
-        const uint32_t S = mine + two * kTok;
-        alive = alive && warp_wait(p, bars + kSFull + two, turn);
+        alive = alive && warp_wait(p, bars + kSFull, t & 1);
         fence_after();
         if (any && alive) {
-          uint32_t r[kTok];
-          tmem_load(S, *reinterpret_cast<uint32_t(*)[32]>(r));
-          tmem_load(S + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-          const float* sc = reinterpret_cast<const float*>(smem + Geo::kScales) + two * 2 * kGroups;
-          const int* live = reinterpret_cast<const int*>(smem + Geo::kLive) + two * kGroups;
-          uint32_t now = ref, see[2];
-          float f[kGroups];
+          const float* sc = reinterpret_cast<const float*>(smem + Geo::kScales) + (t & 1) * 2 * kGroups;
+          const int* live = reinterpret_cast<const int*>(smem + Geo::kLive) + (t & 1) * kGroups;
+          uint32_t now = ref;
 #pragma unroll
-          for (int i = 0; i < kGroups; ++i) now = max(now, pow2_above(sc[kGroups + i])), f[i] = sc[i] * rf;
+          for (int i = 0; i < kGroups; ++i) now = max(now, pow2_above(sc[kGroups + i]));
           const float down = pow2_of(254u - now);
           // which of 32 tokens the row sees
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          auto seen = [&](int c) {
             const int at = base + 32 * c;
-            see[c] = low_bits(pos - at + 1) & (low_bits(live[2 * c]) | (low_bits(live[2 * c + 1]) << 16));
-            if (p.W > 0) see[c] &= ~low_bits(pos - p.W + 1 - at) | low_bits(p.S - at);
-          }
-          const bool all = __all_sync(0xffffffffu, (see[0] & see[1]) == 0xffffffffu);
-          tmem_wait_load();
-          if (!all) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) r[i] = (see[i / 32] >> (i % 32)) & 1u ? r[i] : 0xff800000u;
-          }
-          // scales are not negative, so the largest product of a group gives its largest logit
+            uint32_t see = low_bits(pos - at + 1) & (low_bits(live[2 * c]) | (low_bits(live[2 * c + 1]) << 16));
+            if (p.W > 0) see &= ~low_bits(pos - p.W + 1 - at) | low_bits(p.S - at);
+            return see;
+          };
+          // The tile's maximum.  Loops are not unrolled: a warp alone on its scheduler runs straight code at the rate
+          // at which it is fetched.
           float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_load(mine + 32 * c, r);
+            const uint32_t see = seen(c);
+            const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+            tmem_wait_load();
+            float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (!all) {
 #pragma unroll
-          for (int i = 0; i < kGroups; ++i) {
-            float u[4];
+              for (int i = 0; i < 32; ++i) r[i] = (see >> i) & 1u ? r[i] : 0xff800000u;
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              u[e] = fmaxf(fmaxf(__uint_as_float(r[16 * i + 4 * e]), __uint_as_float(r[16 * i + 4 * e + 1])),
-                           fmaxf(__uint_as_float(r[16 * i + 4 * e + 2]), __uint_as_float(r[16 * i + 4 * e + 3])));
-            const float most = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-            top = fmaxf(top, most == -INFINITY ? -INFINITY : most * f[i]);
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                u[2 * (i / 16) + e] = fmaxf(u[2 * (i / 16) + e], fmaxf(__uint_as_float(r[i + 2 * e]), __uint_as_float(r[i + 2 * e + 1])));
+            // scales are not negative, so the largest product gives the largest logit
+            const float u0 = fmaxf(u[0], u[1]), u1 = fmaxf(u[2], u[3]);
+            top = fmaxf(top, u0 == -INFINITY ? -INFINITY : u0 * (sc[2 * c] * rf));
+            top = fmaxf(top, u1 == -INFINITY ? -INFINITY : u1 * (sc[2 * c + 1] * rf));
           }
           const bool grown = m == -INFINITY ? top > m : top > m + kGrowth;
           if (__any_sync(0xffffffffu, grown || now != ref)) {
             const float mn = grown ? top : m;
-            const float g = mn == m ? 1.f : exp2_fast(m - mn);  // 0 where nothing was seen before
-            l *= g;
-            const float o = g * (pow2_of(ref) * down);
+            const float f = mn == m ? 1.f : exp2_fast(m - mn);  // 0 where nothing was seen before
+            l *= f;
+            const float o = f * (pow2_of(ref) * down);
             if (s > x.s0) {
-              // the outputs of the tile before are done
-              alive = warp_wait(p, bars + kVFree + (two ^ 1), ((t - 1) >> 1) & 1);
-              fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t q[16];
-                tmem_load16(mine + kO + 16 * c, q);
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                tmem_load(mine + kTile + 32 * c, r);
                 tmem_wait_load();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) q[i] = __float_as_uint(__uint_as_float(q[i]) * o);
-                tmem_store16(mine + kO + 16 * c, q);
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * o);
+                tmem_store32(mine + kTile + 32 * c, r);
               }
             }
             m = mn;
             ref = now;
           }
           const float shift = m == -INFINITY ? 0.f : kBase - m;
-          float2 add = make_float2(0.f, 0.f);
-          const float2 nn = make_float2(shift, shift);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[16];
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32], w[16];
+            tmem_load(mine + 32 * c, r);
+            const uint32_t see = seen(c);
+            const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+            const float f0 = sc[2 * c] * rf, f1 = sc[2 * c + 1] * rf, v0 = sc[kGroups + 2 * c] * down, v1 = sc[kGroups + 2 * c + 1] * down;
+            float2 add = make_float2(0.f, 0.f);
+            const float2 nn = make_float2(shift, shift);
+            tmem_wait_load();
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const int grp = 2 * c + i / 16;
-              const float v = sc[kGroups + grp] * down;
-              float2 a = fma2(make_float2(__uint_as_float(r[32 * c + i]), __uint_as_float(r[32 * c + i + 1])), make_float2(f[grp], f[grp]), nn);
+              const float2 ff = i < 16 ? make_float2(f0, f0) : make_float2(f1, f1);
+              const float2 vv = i < 16 ? make_float2(v0, v0) : make_float2(v1, v1);
+              float2 a = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ff, nn);
               a.x = exp2_fast(a.x), a.y = exp2_fast(a.y);
               if (!all) {
-                if (!((see[c] >> i) & 1u)) a.x = 0.f;
-                if (!((see[c] >> (i + 1)) & 1u)) a.y = 0.f;
+                if (!((see >> i) & 1u)) a.x = 0.f;
+                if (!((see >> (i + 1)) & 1u)) a.y = 0.f;
               }
               add = add2(add, a);
-              const float2 b = mul2(a, make_float2(v, v));
+              const float2 b = mul2(a, vv);
               w[i / 2] = pack_half(b.x, b.y);
             }
-            tmem_store16(S + 16 * c, w);
+            l += add.x + add.y;
+            tmem_store16(mine + 16 * c, w);  // over columns of S that every lane of this warp has read
           }
-          l += add.x + add.y;
           tmem_wait_store();
         }
         fence_before();
         rows_sync();  // all of P is there
         if (tid == 0 && ok) {
           fence_after();
-          ok = alive && wait_for(bars + kVFull + two, turn);
-          if (ok) {
-            issue_outputs<D>(sm, bars, tmem, two, s == x.s0);
-            if (s + 1 == x.s1) commit_to(bars + kOFull);
-          } else {
-            raise(p.status, HYB_STATUS_TIMEOUT);
+          ok = issue_outputs<D>(sm, bars, tmem, t, s == x.s0);
+          if (s + 1 < x.s1) {
+            // S takes P's place: not before the products that read it are done
+            ok = ok && wait_for(bars + kVFree, t & 1) && issue_logits<D>(sm, bars, tmem, t + 1);
+          } else if (ok) {
+            commit_to(bars + kOFull);
           }
+          if (!ok) raise(p.status, HYB_STATUS_TIMEOUT);
         }
         __syncwarp();
       }
@@ -526,7 +518,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
         if (x.s0 < x.s1) {
-          tmem_load(mine + kO + 32 * c, r);
+          tmem_load(mine + kTile + 32 * c, r);
           tmem_wait_load();
         } else {
 #pragma unroll
@@ -565,16 +557,15 @@ __global__ void __launch_bounds__(kThreads, kMmaCtasPerSm) paged_mma_kernel(cons
   uint32_t* where = reinterpret_cast<uint32_t*>(smem + Geo::kTmem);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + kSFull + i, 2);
-      mbar_init(bars + kVFull + i, 128);
-      mbar_init(bars + kVFree + i, 1);
-    }
-    mbar_init(bars + kQFull, 128);
+    mbar_init(bars + kKFull, 128);
+    mbar_init(bars + kKFree, 1);
+    mbar_init(bars + kVFull, 128);
+    mbar_init(bars + kVFree, 1);
+    mbar_init(bars + kSFull, 2);
     mbar_init(bars + kOFull, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {  // 256 of the SM's 512 columns
+  if (warp == 0) {  // S and O: 256 of the SM's 512 columns
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(where)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -586,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, kMmaCtasPerSm) paged_mma_kernel(cons
   if (warp < 4)
     softmax_role<D>(p, smem, bars, tmem, tid);
   else
-    convert_role<D, INT8>(p, smem, bars, tmem, tid - 128);
+    convert_role<D, INT8>(p, smem, bars, tid - 128);
   fence_before();
   __syncthreads();
   fence_after();

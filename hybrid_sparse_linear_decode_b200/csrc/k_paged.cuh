@@ -160,6 +160,7 @@ __device__ __forceinline__ Line make_line(const PagedAttnParams& p) {
   l.total = __shfl_sync(0xffffffffu, upto, 31);
   if (p.b.B > 32) {
     uint32_t sum = 0;
+#pragma unroll 1
     for (int b = 32 + lane; b < p.b.B; b += 32) sum += seq_stages<T>(p, b);
     l.total += warp_sum(sum);
   }
@@ -178,6 +179,7 @@ __device__ __forceinline__ int line_find(const PagedAttnParams& p, const Line& l
     return at;
   }
   uint32_t before = __shfl_sync(0xffffffffu, l.before + l.mine, 31);
+#pragma unroll 1
   for (int b0 = 32; b0 < p.b.B; b0 += 32) {
     const uint32_t mine = b0 + lane < p.b.B ? seq_stages<T>(p, b0 + lane) : 0;
     const uint32_t upto = before + warp_upto(mine);

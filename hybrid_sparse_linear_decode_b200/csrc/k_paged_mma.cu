@@ -18,7 +18,6 @@ constexpr int kTile = 128;  // rows, and tokens
 constexpr int kGroups = kTile / 16;
 constexpr int kThreads = 256;
 constexpr float kGrowth = 8.f, kBase = 7.f;
-constexpr uint64_t kLimitNs = 1000000000ull;
 
 template <int D>
 struct MmaGeo {
@@ -91,12 +90,19 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A bounded wait whose first polls do without the timer: reading it takes longer than most waits here.
+// A bounded wait: at most 2^20 polls of at most a microsecond each.  Little code, since every role has a few.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < 4096; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, kLimitNs);
+  for (int i = 0; i < 1 << 20; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
 }
 // A wait of a whole warp: one lane polls.  After a wait that runs out nothing that waits on it is done; the others'
 // waits run out too, and the CTA ends.
@@ -106,6 +112,7 @@ __device__ __forceinline__ bool warp_wait(const PagedAttnParams& p, uint64_t* ba
     ok = wait_for(bar, parity);
     if (!ok) raise(p.status, HYB_STATUS_TIMEOUT);
   }
+  __syncwarp();
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -218,6 +225,7 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
   Piece x;
   start_work(p, w);
   uint32_t t = 0;  // tiles so far
+#pragma unroll 1
   while (next_piece(p, w, x)) {
     if (x.s0 >= x.s1) continue;
     const int32_t* table = p.b.table + (int64_t)x.b * p.b.mp;
@@ -266,6 +274,7 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
     load(p.c.k, c.k);
     load_scales();
     load(p.c.v, c.v);
+#pragma unroll 1
     for (int s = x.s0; s < x.s1; ++s, ++t) {
       const bool more = s + 1 < x.s1;
       if (more) entries(s + 1);
@@ -353,6 +362,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
   start_work(p, w);
   uint32_t t = 0, pieces = 0;
   bool alive = true, ok = true;  // after a wait that ran out the warps keep the barriers' count, and wait for nothing more
+#pragma unroll 1
   while (next_piece(p, w, x)) {
     const int row = x.row0 + tid, pos0 = x.seq.len - x.seq.n;
     const bool there = row < x.rows, any = x.row0 + 32 * warp < x.rows;
@@ -397,6 +407,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
         ok = issue_logits<D>(sm, bars, tmem, t);
         if (!ok) raise(p.status, HYB_STATUS_TIMEOUT);
       }
+#pragma unroll 1
       for (int s = x.s0; s < x.s1; ++s, ++t) {
         int base, end;
         stage_range(x.span, s, base, end);

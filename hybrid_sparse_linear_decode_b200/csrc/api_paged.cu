@@ -58,6 +58,7 @@ bool rows_ok(const void* p, int64_t stride, int64_t heads, int d, int64_t unit) 
 struct Plan {
   enum Form { kNarrow, kWide, kMma } form;
   int rows;      // of the line's units: narrow 8, 16, 32 or 64, mma 128; 0 with splits
+  int cluster;   // CTAs a unit (narrow), or 0
   int n_cta;     // line
   int n_splits;  // otherwise
   size_t bytes;
@@ -68,8 +69,9 @@ struct Plan {
 // products (narrow up to 64 rows, then wide).  While a sequence's rows fit one tile the CTAs share the line of all
 // tiles; more rows, and few row tiles, cut each row tile's tokens into as many parts as fill the SMs, each of at least
 // kLeastTokens.
-constexpr int kNarrowMost = 16;
+constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
+constexpr int kClusterStages = 32;
 
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink, int type) {
   Plan p{};
@@ -88,6 +90,15 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
     const int64_t stage = mma ? 128 : 32, warps = mma ? 1 : 4;
     const int64_t stages = std::max<int64_t>(1, (len + stage - 1) / stage);
     p.rows = mma ? tile : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (!mma) {
+      // each CTA's part of a unit: a stage for each of its warps at least, all units' CTAs on the SMs at once if they
+      // can; short enough that the rest of the time is latency
+      const int64_t most = std::min<int64_t>({kPagedMaxCluster, std::max<int64_t>(1, kSms * kCtasPerSm / units), (stages + 3) / 4});
+      if ((stages + most - 1) / most <= kClusterStages) {
+        p.cluster = (int)most;
+        return p;
+      }
+    }
     p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * (mma ? kMmaCtasPerSm : kCtasPerSm), (units * stages + warps - 1) / warps));
     p.bytes = (size_t)2 * p.n_cta * p.rows * row_bytes;
   } else {
@@ -187,6 +198,7 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   p.W = window;
   p.S = window > 0 ? n_sink : 0;
   p.scale = (scale > 0.f ? scale : 1.f / sqrtf((float)d)) * 1.44269504088896341f;
+  p.cluster = plan.cluster;
   p.n_cta = plan.n_cta;
   p.quantum = plan.form == Plan::kMma ? 1 : 4;
   p.n_splits = plan.n_splits;

@@ -393,7 +393,29 @@ __device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, floa
 // line that the CTAs cut into equal parts, so ragged batches keep every SM busy
 // to the end; the teams of a CTA (one, two or four warps that share a ring, with 8 or
 // 16 rows each) take its stages in turn and are joined at each unit's end.  A unit that
-// more than one CTA worked on is joined by paged_join_kernel.
+// more than one CTA worked on is joined by paged_join_kernel.  Short sequences are bound by
+// latency instead: a cluster of CTAs takes each unit and joins it itself, in one launch.
+
+constexpr int kMaxCluster = kPagedMaxCluster;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared memory `at` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t in_rank(uint32_t at, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 load_rank2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_rank4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
 template <int GW>
 __device__ __forceinline__ void team_sync() {
@@ -418,23 +440,42 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
   uint8_t* ring = smem + team * kRing * kBytes;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
 
-  const Line line = make_line<kStageTokens>(p);
-  const uint32_t first = min(line.per * blockIdx.x, line.total), last = min(first + line.per, line.total);
-  uint32_t at = first;
-  pdl_allow_dependents();  // the join may take its place; it waits for this grid's end
+  // A cluster (p.cluster CTAs) takes one unit, its CTAs equal parts of it; otherwise CTAs take parts of the line.
+  Line line{};
+  uint32_t first = 0, last = 1, at = 0;
+  if (p.cluster == 0) {
+    line = make_line<kStageTokens>(p);
+    first = at = min(line.per * blockIdx.x, line.total);
+    last = min(first + line.per, line.total);
+    pdl_allow_dependents();  // the join may take its place; it waits for this grid's end
+  }
   while (at < last) {
-    // the unit that stage `at` lies in, and the part of it that is this CTA's
-    uint32_t begin;
-    const int b = line_find<kStageTokens>(p, line, at, begin);
-    bool bad;
-    const Seq seq = read_seq(p.b, b, p.c.P, &bad);
-    const Span<kStageTokens> span = seq_span<kStageTokens>(p, seq);
-    const int h = (int)((at - begin) / (uint32_t)span.stages);
-    const uint32_t ubegin = begin + (uint32_t)h * span.stages;
-    const int s0 = (int)(at - ubegin), s1 = (int)min((uint32_t)span.stages, last - ubegin);
-    const bool complete = s0 == 0 && s1 == span.stages;
-    const int slot = 2 * blockIdx.x + (at == first ? 0 : 1);
-    at = ubegin + s1;
+    int b, h, s0, s1, slot = 0;
+    bool bad, complete;
+    Seq seq;
+    Span<kStageTokens> span;
+    if (p.cluster == 0) {
+      // the unit that stage `at` lies in, and the part of it that is this CTA's
+      uint32_t begin;
+      b = line_find<kStageTokens>(p, line, at, begin);
+      seq = read_seq(p.b, b, p.c.P, &bad);
+      span = seq_span<kStageTokens>(p, seq);
+      h = (int)((at - begin) / (uint32_t)span.stages);
+      const uint32_t ubegin = begin + (uint32_t)h * span.stages;
+      s0 = (int)(at - ubegin), s1 = (int)min((uint32_t)span.stages, last - ubegin);
+      complete = s0 == 0 && s1 == span.stages;
+      slot = 2 * blockIdx.x + (at == first ? 0 : 1);
+      at = ubegin + s1;
+    } else {
+      const int unit = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+      b = unit / p.c.Hkv, h = unit % p.c.Hkv;
+      seq = read_seq(p.b, b, p.c.P, &bad);
+      span = seq_span<kStageTokens>(p, seq);
+      const int part = (span.stages + p.cluster - 1) / p.cluster;
+      s0 = min(part * rank, span.stages), s1 = min(s0 + part, span.stages);
+      complete = p.cluster == 1;
+      at = last;
+    }
     const int rows = min(seq.n * p.G, kRows), pos0 = seq.len - seq.n;
     const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
     if (bad && h == 0 && s0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
@@ -514,12 +555,47 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
       if (complete) {
         store_joined(p, seq.t0 + row / p.G, h * p.G + row % p.G, D, c / 4, y, m, l);
       } else {
-        float* ws = p.ws + ((int64_t)slot * kRows + row) * (D + 4);
-        *reinterpret_cast<float4*>(ws + c) = y;
-        if (c == 0) *reinterpret_cast<float2*>(ws + D) = make_float2(m, l);
+        float* to = p.cluster > 0 ? body + (kTeams * kRows + row) * kRowFloats : p.ws + ((int64_t)slot * kRows + row) * (D + 4);
+        *reinterpret_cast<float4*>(to + c) = y;
+        if (c == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, l);
       }
     }
     __syncthreads();
+    if (p.cluster > 1) {
+      // Join the cluster's parts: its CTAs take the row's pieces in turn, and read each other's shared memory.
+      cluster_sync();
+      const int rank = blockIdx.x % p.cluster;
+      const uint32_t parts = smem_u32(body + kTeams * kRows * kRowFloats);
+      for (int x = rank * kWarps * 32 + threadIdx.x; x < rows * (D / 4); x += p.cluster * kWarps * 32) {
+        const int row = x / (D / 4), c = x % (D / 4) * 4;
+        float4 o[kMaxCluster];
+        float2 e[kMaxCluster];
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
+          e[i] = make_float2(-INFINITY, 0.f);
+          o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < p.cluster) {
+            const uint32_t from = in_rank(parts + row * kRowFloats * 4, i);
+            e[i] = load_rank2(from + D * 4);
+            o[i] = load_rank4(from + c * 4);
+          }
+          m = fmaxf(m, e[i].x);
+        }
+        float l = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
+          const float w = m == -INFINITY ? 0.f : exp2_fast(e[i].x - m) * e[i].y;
+          l += w;
+          y.x += w * o[i].x, y.y += w * o[i].y, y.z += w * o[i].z, y.w += w * o[i].w;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+        store_joined(p, seq.t0 + row / p.G, h * p.G + row % p.G, D, c / 4, y, m, l);
+      }
+      cluster_sync();  // no CTA ends while another reads its memory
+    }
   }
 }
 
@@ -742,9 +818,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_rows_kernel(const Pag
 template <int D, bool INT8, int NT, int GW, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
   constexpr int kRows = 8 * NT * GW;
-  constexpr size_t smem = (size_t)NarrowGeo<D, GW>::kTeams * NarrowGeo<D, GW>::kStages * StageGeo<D>::kBytes;
-  static_assert(smem >= (size_t)NarrowGeo<D, GW>::kTeams * kRows * (D + 4) * sizeof(float), "the joined rows fit the rings");
-  cudaError_t e = launch(paged_narrow_kernel<D, INT8, NT, GW, FINE>, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
+  constexpr size_t rings = (size_t)NarrowGeo<D, GW>::kTeams * NarrowGeo<D, GW>::kStages * StageGeo<D>::kBytes;
+  constexpr size_t rows = (size_t)(NarrowGeo<D, GW>::kTeams + 1) * kRows * (D + 4) * sizeof(float);
+  constexpr size_t smem = rings > rows ? rings : rows;
+  static_assert(smem <= 74 * 1024, "three CTAs share an SM");
+  const auto kernel = paged_narrow_kernel<D, INT8, NT, GW, FINE>;
+  if (p.cluster > 0) return launch_clusters(kernel, dim3(p.b.B * p.c.Hkv * p.cluster), p.cluster, dim3(kWarps * 32), smem, s, p);
+  cudaError_t e = launch(kernel, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
   if (e != cudaSuccess) return e;
   const int n = p.b.max_new * p.G < kRows ? p.b.max_new * p.G : kRows;
   return launch(paged_join_kernel<D, kStageTokens>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, kRows);

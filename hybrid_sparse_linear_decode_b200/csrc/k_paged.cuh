@@ -230,5 +230,25 @@ cudaError_t launch(void (*f)(A...), dim3 grid, dim3 block, size_t smem, bool cha
   return cudaLaunchKernelEx(&c, f, args...);
 }
 
+template <class... A>
+cudaError_t launch_clusters(void (*f)(A...), dim3 grid, int cluster, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&c, f, args...);
+}
+
 }  // namespace
 }  // namespace hyb

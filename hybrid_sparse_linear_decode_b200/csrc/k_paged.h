@@ -49,6 +49,7 @@ struct PagedAttnParams {
   int64_t q_stride, out_stride;
   int32_t Hq, G, half, W, S;
   float scale;       // times log2(e)
+  int32_t cluster;   // CTAs of a cluster that takes one unit (narrow form), or 0
   int32_t n_cta;     // CTAs that share the line of all units' stages
   int32_t quantum;   // stages that a CTA's part is a multiple of
   int32_t n_splits;  // parts of each row tile's stages (wide forms)
@@ -61,6 +62,7 @@ struct PagedAttnParams {
 constexpr int kNarrowRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kCtasPerSm = 3;
+constexpr int kPagedMaxCluster = 8;  // a portable size
 // Rows of a CTA of the form on tcgen05.
 constexpr int kMmaRows = 128;
 constexpr int kMmaCtasPerSm = 2;

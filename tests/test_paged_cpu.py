@@ -148,8 +148,8 @@ def test_attend_refuses_bad_rows(A, kw, code):
     a = dict(type=0, q=256, q_stride=256, out=512, out_stride=256, lse=None, n_q_heads=4, window=0, n_sink=0, scale=0.0,
              workspace=1024, workspace_bytes=1 << 30, stream=None)
     a.update(kw)
-    with pytest.raises(A.HybAttnError) as e:
-        A.hyb_attn_paged_attend(_cache(A), _batch(A), **a)
+    with pytest.raises(A.HybAttnError) as e:   # long enough that the parts of a sequence go through the workspace
+        A.hyb_attn_paged_attend(_cache(A), _batch(A, table_stride=4096, max_len=65536), **a)
     assert e.value.code == code
 
 

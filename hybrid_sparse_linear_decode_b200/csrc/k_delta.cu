@@ -54,6 +54,8 @@ struct Piece {
 template <int DK>
 __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
   constexpr int kRows = DK / 4;  // of a lane
+  pdl_wait_primary();
+  pdl_allow_dependents();
   const int b = blockIdx.x / p.Hv, hv = blockIdx.x % p.Hv, hk = hv / (p.Hv / p.Hk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = (lane >> 3) * kRows, col = warp * 32 + (lane & 7) * 4;
@@ -456,6 +458,8 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(ChunkGeo<DK, DV>::kThreads, 1) delta_chunks_kernel(const DeltaParams p) {
   using Geo = ChunkGeo<DK, DV>;
   extern __shared__ __align__(128) uint8_t smem[];
+  pdl_wait_primary();
+  pdl_allow_dependents();
   const int b = blockIdx.x / p.Hv, hv = blockIdx.x % p.Hv, hk = hv / (p.Hv / p.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const Run run = read_run(p, b, hv == 0 && tid == 0);
@@ -666,23 +670,33 @@ __global__ void __launch_bounds__(ChunkGeo<DK, DV>::kThreads, 1) delta_chunks_ke
       state[(int64_t)(8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] = S[j][e] * unit[e >> 1];
 }
 
+cudaError_t launch(void (*f)(DeltaParams), int blocks, int threads, int smem, const DeltaParams& p, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, f, p);
+}
+
 template <int DK, int DV>
 cudaError_t chunks(const DeltaParams& p, cudaStream_t s) {
-  constexpr int smem = ChunkGeo<DK, DV>::kTotal;
-  const cudaError_t e = cudaFuncSetAttribute(delta_chunks_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  delta_chunks_kernel<DK, DV><<<p.B * p.Hv, ChunkGeo<DK, DV>::kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch(delta_chunks_kernel<DK, DV>, p.B * p.Hv, ChunkGeo<DK, DV>::kThreads, ChunkGeo<DK, DV>::kTotal, p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_steps(const DeltaParams& p, cudaStream_t s) {
-  if (p.DK == 128)
-    delta_steps_kernel<128><<<p.B * p.Hv, p.DV, 0, s>>>(p);
-  else
-    delta_steps_kernel<64><<<p.B * p.Hv, p.DV, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch(p.DK == 128 ? delta_steps_kernel<128> : delta_steps_kernel<64>, p.B * p.Hv, p.DV, 0, p, s);
 }
 
 cudaError_t launch_delta_chunks(const DeltaParams& p, cudaStream_t s) {

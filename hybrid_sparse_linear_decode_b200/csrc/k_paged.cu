@@ -435,6 +435,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
   constexpr int kRows = 8 * NT * GW;
   // a joined row's place: D floats and 4 more, so that rows begin in different banks
   constexpr int kRowFloats = D + 4;
+  pdl_wait_primary();
+  pdl_allow_dependents();  // they wait for this grid's end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int team = warp / GW, member = warp % GW, me = threadIdx.x % (GW * 32);
   uint8_t* ring = smem + team * kRing * kBytes;
@@ -447,7 +449,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
     line = make_line<kStageTokens>(p);
     first = at = min(line.per * blockIdx.x, line.total);
     last = min(first + line.per, line.total);
-    pdl_allow_dependents();  // the join may take its place; it waits for this grid's end
   }
   while (at < last) {
     int b, h, s0, s1, slot = 0;
@@ -718,6 +719,8 @@ template <int D, bool INT8, bool FINE>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int NT = 2, kBytes = StageGeo<D>::kBytes, kRowFloats = D + 4;
+  pdl_wait_primary();
+  pdl_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t magic = (uint32_t)(((1ull << 32) + p.c.P / 16 - 1) / (uint32_t)(p.c.P / 16));
   const int unit = blockIdx.y, b = unit / p.c.Hkv, h = unit % p.c.Hkv;
@@ -824,7 +827,7 @@ cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
   static_assert(smem <= 74 * 1024, "three CTAs share an SM");
   const auto kernel = paged_narrow_kernel<D, INT8, NT, GW, FINE>;
   if (p.cluster > 0) return launch_clusters(kernel, dim3(p.b.B * p.c.Hkv * p.cluster), p.cluster, dim3(kWarps * 32), smem, s, p);
-  cudaError_t e = launch(kernel, dim3(p.n_cta), dim3(kWarps * 32), smem, false, s, p);
+  cudaError_t e = launch(kernel, dim3(p.n_cta), dim3(kWarps * 32), smem, true, s, p);
   if (e != cudaSuccess) return e;
   const int n = p.b.max_new * p.G < kRows ? p.b.max_new * p.G : kRows;
   return launch(paged_join_kernel<D, kStageTokens>, dim3(p.b.B * p.c.Hkv, n), dim3(kJoinThreads), 0, true, s, p, kRows);
@@ -845,7 +848,7 @@ cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   static_assert(smem >= (size_t)kWarps * 8 * (D + 4) * sizeof(float), "the rows that leave fit");
   const int64_t tiles = ((int64_t)p.b.max_new * p.G + kWideRows - 1) / kWideRows;
   cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
-                         dim3(kWarps * 32), smem, false, s, p);
+                         dim3(kWarps * 32), smem, true, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   return launch_paged_join_rows(p, D, s);
 }

@@ -171,12 +171,16 @@ __device__ __forceinline__ void rotate_queries(const PagedAppendParams& p, int64
 
 template <bool INTERLEAVED, bool HALF>
 __global__ void __launch_bounds__(kRotateThreads, 4) paged_rotate_kernel(const PagedAppendParams p) {
+  pdl_wait_primary();
+  pdl_allow_dependents();
   rotate_queries<INTERLEAVED, HALF>(p, (int64_t)blockIdx.x * kRotateThreads + threadIdx.x);
 }
 
 template <bool INTERLEAVED, bool HALF, bool INT8>
 __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendParams p) {
   constexpr bool half = HALF;
+  pdl_wait_primary();
+  pdl_allow_dependents();
   const int lanes = p.D / 16;  // lanes of a row: 4 or 8
   const int P = p.c.P;
 
@@ -311,10 +315,10 @@ cudaError_t append(const PagedAppendParams& p, cudaStream_t s) {
   const bool apart = q_threads >= kRotateApart;
   const int64_t blocks = p.kv_blocks + (apart ? 0 : (q_threads + threads - 1) / threads);
   const cudaError_t e = launch(p.int8 ? paged_append_kernel<INTERLEAVED, HALF, true> : paged_append_kernel<INTERLEAVED, HALF, false>,
-                               dim3((unsigned)blocks), dim3(threads), 0, false, s, p);
+                               dim3((unsigned)blocks), dim3(threads), 0, true, s, p);
   if (!apart || e != cudaSuccess) return e;
   return launch(paged_rotate_kernel<INTERLEAVED, HALF>, dim3((unsigned)((q_threads + kRotateThreads - 1) / kRotateThreads)),
-                dim3(kRotateThreads), 0, false, s, p);
+                dim3(kRotateThreads), 0, true, s, p);
 }
 }  // namespace
 

@@ -563,6 +563,7 @@ template <int D, bool INT8>
 __global__ void __launch_bounds__(kThreads, kMmaCtasPerSm) paged_mma_kernel(const PagedAttnParams p) {
   using Geo = MmaGeo<D>;
   extern __shared__ uint8_t raw[];
+  pdl_wait_primary();
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo::kBars);
   uint32_t* where = reinterpret_cast<uint32_t*>(smem + Geo::kTmem);
@@ -602,7 +603,7 @@ cudaError_t run(const PagedAttnParams& p, cudaStream_t s) {
     const int64_t tiles = ((int64_t)p.b.max_new * p.G + kTile - 1) / kTile;
     grid = dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv);
   }
-  return launch(paged_mma_kernel<D, INT8>, grid, dim3(kThreads), MmaGeo<D>::kTotal, false, s, p);
+  return launch(paged_mma_kernel<D, INT8>, grid, dim3(kThreads), MmaGeo<D>::kTotal, true, s, p);
 }
 
 }  // namespace

@@ -159,27 +159,40 @@ struct Queries {
   uint2 frag[NT][D / 16];
 };
 
-// Loads the fragments of rows row_first .., and the rows' factors and positions.
+// The query rows' bits, under way while the first stages are found: channels 16 t .. + 15 (and 64 more) of row g.
 template <int D, int NT>
-__device__ __forceinline__ void load_rows(const PagedAttnParams& p, Queries<D, NT>& Q, Rows<D, NT>& R, int t0, int h,
-                                          int row_first, int rows, int pos0) {
+struct RawRows {
+  uint4 z[NT][D / 64][2];
+};
+template <int D, int NT>
+__device__ __forceinline__ void fetch_rows(const PagedAttnParams& p, RawRows<D, NT>& raw, int t0, int h, int row_first, int rows) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool half = p.half != 0;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int row = row_first + 8 * n + g;
     const bool there = row < rows;
     const int tok = there ? row / p.G : 0, head = there ? row % p.G : 0;
     const uint16_t* src = p.q + (int64_t)(t0 + tok) * p.q_stride + (int64_t)(h * p.G + head) * D + 16 * t;
+#pragma unroll
+    for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        raw.z[n][hh][e] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * hh) + e) : make_uint4(0, 0, 0, 0);
+  }
+}
+// Their fragments, factors and positions.
+template <int D, int NT>
+__device__ __forceinline__ void make_rows(const PagedAttnParams& p, const RawRows<D, NT>& raw, Queries<D, NT>& Q, Rows<D, NT>& R,
+                                          int row_first, int rows, int pos0) {
+  const int t = threadIdx.x & 3;
+  const bool half = p.half != 0;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     float x[D / 64][16];
     float amax = 0.f;
 #pragma unroll
     for (int hh = 0; hh < D / 64; ++hh) {
-      uint4 u = make_uint4(0, 0, 0, 0), w = u;
-      if (there) {
-        u = __ldg(reinterpret_cast<const uint4*>(src + 64 * hh));
-        w = __ldg(reinterpret_cast<const uint4*>(src + 64 * hh) + 1);
-      }
+      const uint4 u = raw.z[n][hh][0], w = raw.z[n][hh][1];
       const uint32_t z[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -481,7 +494,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
     const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
     if (bad && h == 0 && s0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
 
-    // start the first stages, then the queries
+    // the queries, then the first stages
+    RawRows<D, NT> raw;
+    fetch_rows<D, NT>(p, raw, seq.t0, h, 8 * NT * member, rows);
     const int mine = s1 - s0 > team ? (s1 - s0 - team + kTeams - 1) / kTeams : 0;
     StagePages nxt;
     int base, end;
@@ -501,7 +516,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
     Rows<D, NT> R;
     Queries<D, NT> Q;
     R.clear();
-    load_rows<D, NT>(p, Q, R, seq.t0, h, 8 * NT * member, rows, pos0);
+    make_rows<D, NT>(p, raw, Q, R, 8 * NT * member, rows, pos0);
 
     int slot_in = kRing - 1, slot_out = 0;
     for (int i = 0; i < mine; ++i) {
@@ -738,6 +753,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
   const int s1 = (int)((int64_t)span.stages * (split + 1) / p.n_splits);
   const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
 
+  RawRows<D, NT> raw;
+  fetch_rows<D, NT>(p, raw, seq.t0, h, row0 + 8 * NT * warp, rows);
   StagePages nxt;
   int base, end;
   auto find = [&](int i) {
@@ -756,7 +773,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
   Rows<D, NT> R;
   Queries<D, NT> Q;
   R.clear();
-  load_rows<D, NT>(p, Q, R, seq.t0, h, row0 + 8 * NT * warp, rows, pos0);
+  make_rows<D, NT>(p, raw, Q, R, row0 + 8 * NT * warp, rows, pos0);
   for (int i = s0; i < s1; ++i) {
     cp_wait<kWideRing - 2>();
     __syncthreads();  // the stage is there, and everyone is done with the one before

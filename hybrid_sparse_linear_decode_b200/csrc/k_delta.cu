@@ -1,8 +1,12 @@
 // The gated delta rule: S := a S, S := S + k (beta (v - S^T k))^T, o = scale S^T q, a = exp(g).
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "hyb_device.cuh"
 #include "k_delta.h"
+#include "k_tcgen05.cuh"
 
 namespace hyb {
 namespace {
@@ -138,34 +142,31 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
 // them.  Only O, whose result has 8 bits, takes single parts of S, U and P.  Sums are in 32 bits.  Errors of the
 // state stay near those of 32-bit arithmetic.
 
-constexpr int kC = 64;
+constexpr int kC = 64, kChunkThreads = 512;  // eight scanning warps, two groups of four that prepare
 
-template <int DK, int DV>
+template <int DK>
 struct ChunkGeo {
-  static constexpr int kScan = DV / 16, kPrep = 4;  // warps
-  static constexpr int kThreads = (kScan + kPrep) * 32;
-  // one chunk: K, Q [64][DK] f16, V [64][DV] bf16, T [64][64] in two parts, P [64][64], and seven rows of 64 factors
-  static constexpr int kK = 0, kQ = kK + kC * DK * 2, kV = kQ + kC * DK * 2, kT = kV + kC * DV * 2, kP = kT + 2 * kC * kC * 2,
-                       kE = kP + kC * kC * 2, kBytes = kE + 7 * kC * 4;
+  // one chunk: K, Q [64][DK] f16, T [64][64] in two parts, P [64][64], and seven rows of 64 factors
+  static constexpr int kK = 0, kQ = kK + kC * DK * 2, kT = kQ + kC * DK * 2, kP = kT + 2 * kC * kC * 2, kE = kP + kC * kC * 2,
+                       kBytes = kE + 2048;
+  // three of them; each group's A, products of blocks and sums of g; columns' maxima; barriers; the tensor memory's address
   static constexpr int kLd = kC + 4;  // row of A in floats
-  static constexpr int kA = 2 * kBytes, kTmp = kA + kC * kLd * 4, kG = kTmp + 32 * 36 * 4, kTotal = kG + 3 * kC * 4;
+  static constexpr int kTmp = kC * kLd * 4, kG = kTmp + 32 * 36 * 4, kWorkBytes = kG + 3 * kC * 4;
+  static constexpr int kWork = 3 * kBytes, kMost = kWork + 2 * kWorkBytes, kBars = kMost + 2 * 2 * 128 * 4, kTmem = kBars + 16 * 8,
+                       kTotal = kTmem + 16 + 1024;  // 1024: the tiles begin at a multiple of it
 };
+// Barriers: a place is full, free; products of a chunk are done
+enum { kFull, kFree = 3, kDoneX = 6, kDoneU, kDoneS };
+// Columns of the tensor memory: S^T; as f16, upper and lower halves; X^T, then U^T; Q S; W or U in two parts; P U
+enum { kColS = 0, kColSh = 128, kColSl = 192, kColX = 256, kColQ = 320, kColW = 384, kColP = 448 };
 // The factors' rows: e^G; beta e^G kappa; beta; kappa; e^(G_C - G); scale kappa of q; e^G_C
 enum { kDecay, kForget, kBeta, kKappa, kLeft, kOut, kWhole };
 
-// Byte offset of 16-byte piece c of row r in a tile with rows of `pieces` pieces: moved so that 8 rows' pieces of one
-// column lie in different banks.
-template <int PIECES>
-__device__ __forceinline__ int tile_at(int r, int c) {
-  return (r * PIECES + (c ^ (r & 7))) * 16;
-}
+// Byte offset of 16-byte piece c of row r in tiles of 64 rows of 8 pieces, moved so that 8 rows' pieces of one column lie
+// in different banks (the tensor cores' 128-byte swizzle).
+__device__ __forceinline__ int tile_at(int r, int c) { return (c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) * 16); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -182,18 +183,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   lo = pack_half(x - b.x, y - b.y);
 }
-// The left operand of a k-step from two accumulator tiles.
-__device__ __forceinline__ void split_a(const float (&c)[4], const float (&d)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split2(c[0], c[1], hi[0], lo[0]);
-  split2(c[2], c[3], hi[1], lo[1]);
-  split2(d[0], d[1], hi[2], lo[2]);
-  split2(d[2], d[3], hi[3], lo[3]);
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -204,71 +193,68 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 __device__ __forceinline__ uint32_t field_of(float x, uint32_t lo, uint32_t hi) { return min(max(__float_as_uint(x) >> 23, lo), hi); }
 __device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
 
-// Rows of K or Q: loaded, divided by their kappa and stored as f16.  16-byte pieces of a row lie in DK / 8 lanes.
-template <int DK, int N>
-struct RowPieces {
-  uint4 w[N];
-  __device__ __forceinline__ void load(const uint16_t* src, int64_t stride, int row, int n, int tid) {
-    constexpr int kPieces = DK / 8;
+// Rows of K or Q, four 16-byte pieces of each thread at a time: loaded, and divided by their kappa and stored as f16.
+// The pieces of a row lie in DK / 8 lanes.
+template <int DK>
+__device__ __forceinline__ void load_rows(uint4 (&w)[4], const uint16_t* src, int64_t stride, int n, int first, int tid) {
+  constexpr int kPieces = DK / 8;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = tid + 128 * i, r = at / kPieces, c = at % kPieces;
-      w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(row + r) * stride + c * 8)) : make_uint4(0, 0, 0, 0);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int at = tid + 128 * (first + i), r = at / kPieces, c = at % kPieces;
+    w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + r * stride + c * 8)) : make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void store(uint8_t* tile, float* kappa, int tid) {
-    constexpr int kPieces = DK / 8;
+}
+template <int DK>
+__device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, float* kappa, int first, int tid) {
+  constexpr int kPieces = DK / 8;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = tid + 128 * i, r = at / kPieces, c = at % kPieces;
-      const uint32_t z[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      uint32_t top = 0;  // magnitudes of bf16 order as integers
+  for (int i = 0; i < 4; ++i) {
+    const int at = tid + 128 * (first + i), r = at / kPieces, c = at % kPieces;
+    const uint32_t z[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t both = 0;  // magnitudes of bf16 order as integers
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(z[e] & 0x7fffu, (z[e] >> 16) & 0x7fffu));
+    for (int e = 0; e < 4; ++e) both = __vmaxu2(both, z[e] & 0x7fff7fffu);
 #pragma unroll
-      for (int o = 1; o < kPieces; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const uint32_t e = min(max(top >> 7, 1u), 253u);
-      const float inv = pow2_of(254u - e);
-      uint32_t y[4];
+    for (int o = 1; o < kPieces; o <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const uint32_t e = min(max(max(both & 0xffffu, both >> 16) >> 7, 1u), 253u);
+    const float inv = pow2_of(254u - e);
+    uint32_t y[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) y[x] = pack_half(bf16_lo(z[x]) * inv, bf16_hi(z[x]) * inv);
-      *reinterpret_cast<uint4*>(tile + tile_at<kPieces>(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
-      if (c == 0) kappa[r] = pow2_of(e);
-    }
+    for (int x = 0; x < 4; ++x) y[x] = pack_half(bf16_lo(z[x]) * inv, bf16_hi(z[x]) * inv);
+    *reinterpret_cast<uint4*>(tile + tile_at(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (c == 0) kappa[r] = pow2_of(e);
   }
-};
+}
 
-template <int DK, int DV>
-__device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* smem, uint8_t* buf, int row, int n, int next, int hk, int hv, int tid) {
-  using Geo = ChunkGeo<DK, DV>;
-  constexpr int kLd = Geo::kLd, kPieces = DK / 8;
+// Prepares the chunk of n tokens from `row` on in `buf`; this group's next one has `next` tokens from row `ahead` on.
+template <int DK>
+__device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* smem, uint8_t* buf, int barrier, int row, int n, int ahead,
+                                              int next, int hk, int hv, int tid) {
+  using Geo = ChunkGeo<DK>;
+  constexpr int kLd = Geo::kLd;
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t sm = smem_u32(buf);
   float* E = reinterpret_cast<float*>(buf + Geo::kE);
   float* Ghi = reinterpret_cast<float*>(smem + Geo::kG);
   float* Glo = Ghi + kC;
   float* kq = Glo + kC;
-  // the chunk's rows; past its end zeros
-  RowPieces<DK, DK / 16> K, Q;
-  K.load(p.k + (int64_t)hk * DK, p.k_stride, row, n, tid);
-  Q.load(p.q + (int64_t)hk * DK, p.q_stride, row, n, tid);
-#pragma unroll
-  for (int i = tid; i < kC * (DV / 8); i += 128) {
-    const int r = i / (DV / 8), c = i % (DV / 8);
-    const bool there = r < n;
-    cp_async16(sm + Geo::kV + tile_at<DV / 8>(r, c), p.v + (int64_t)(row + (there ? r : 0)) * p.v_stride + (int64_t)hv * DV + c * 8,
-               there ? 16 : 0);
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  // the chunk after this one on its way into L2, a line of 128 bytes at a time
+  // the chunk's rows, past its end zeros: K's four pieces at a time, then Q's
+  constexpr int kSteps = DK / 64;  // of each
+  const uint16_t* from_k = p.k + (int64_t)row * p.k_stride + (int64_t)hk * DK;
+  const uint16_t* from_q = p.q + (int64_t)row * p.q_stride + (int64_t)hk * DK;
+  uint4 rows[4];
+  load_rows<DK>(rows, from_k, p.k_stride, n, 0, tid);
+  // the next chunk on its way into L2, a line of 128 bytes at a time
   for (int i = tid; i < next * (DK / 64); i += 128) {
-    const int64_t r = row + kC + i / (DK / 64);
+    const int64_t r = ahead + i / (DK / 64);
     const int c = i % (DK / 64) * 64;
     prefetch_l2(p.k + r * p.k_stride + (int64_t)hk * DK + c);
     prefetch_l2(p.q + r * p.q_stride + (int64_t)hk * DK + c);
   }
-  for (int i = tid; i < next * (DV / 64); i += 128)
-    prefetch_l2(p.v + (int64_t)(row + kC + i / (DV / 64)) * p.v_stride + (int64_t)hv * DV + i % (DV / 64) * 64);
+  for (int i = tid; i < next * (p.DV / 64); i += 128) {
+    const int lines = p.DV / 64;
+    prefetch_l2(p.v + (int64_t)(ahead + i / lines) * p.v_stride + (int64_t)hv * p.DV + i % lines * 64);
+  }
   // the sums of g in powers of two and in 64 bits, kept as two floats so that their differences keep 32; a
   // decay of e^-200 is 0 in 32 bits like any stronger one.  Two tokens a lane.
   const int r0 = 2 * lane, r1 = r0 + 1;
@@ -293,10 +279,17 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     E[kBeta * kC + r0] = b0, E[kBeta * kC + r1] = b1;
     if (lane == 0) E[kWhole * kC] = exp2f((float)end);
   }
-  K.store(buf + Geo::kK, E + kKappa * kC, tid);
-  Q.store(buf + Geo::kQ, kq, tid);
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  bar_sync(5, 128);
+#pragma unroll 1
+  for (int i = 0; i < 2 * kSteps; ++i) {
+    const bool of_q = i >= kSteps, then_q = i + 1 >= kSteps;
+    uint4 then[4];
+    if (i + 1 < 2 * kSteps)
+      load_rows<DK>(then, then_q ? from_q : from_k, then_q ? p.q_stride : p.k_stride, n, 4 * ((i + 1) % kSteps), tid);
+    store_rows<DK>(rows, buf + (of_q ? Geo::kQ : Geo::kK), of_q ? kq : E + kKappa * kC, 4 * (i % kSteps), tid);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) rows[x] = then[x];
+  }
+  bar_sync(barrier, 128);
   if (warp == 0) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -306,59 +299,49 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     }
   }
 
-  // K K^T and Q K^T: this warp's 16 rows against the columns up to them
-  float* A = reinterpret_cast<float*>(smem + Geo::kA);
-  float kk[8][4], qk[8][4];
+  // K K^T and Q K^T below the diagonal, in blocks of 16 x 16: first this warp's own on the diagonal, then the six others in turn
+  float* A = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+  for (int i = warp; i < 10; i += 4) {
+    const int bi = i < 4 ? i : i == 4 ? 1 : i < 7 ? 2 : 3, bj = i < 4 ? i : i == 4 ? 0 : i < 7 ? i - 5 : i - 7;
+    float kk[2][4], qk[2][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
-  const int tiles = 2 * warp + 2;
+      for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
 #pragma unroll 2
-  for (int ks = 0; ks < DK / 16; ks += 2) {
-    uint32_t a[2][4], c[2][4];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int at = tile_at<kPieces>(16 * warp + (lane & 15), 2 * (ks + x) + (lane >> 4));
-      ldsm_x4(sm + Geo::kK + at, a[x][0], a[x][1], a[x][2], a[x][3]);
-      ldsm_x4(sm + Geo::kQ + at, c[x][0], c[x][1], c[x][2], c[x][3]);
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t a[4], c[4], b[4];
+      const int at = tile_at(16 * bi + (lane & 15), 2 * ks + (lane >> 4));
+      ldsm_x4(sm + Geo::kK + at, a[0], a[1], a[2], a[3]);
+      ldsm_x4(sm + Geo::kQ + at, c[0], c[1], c[2], c[3]);
+      ldsm_x4(sm + Geo::kK + tile_at(16 * bj + (lane & 7) + 8 * (lane >> 4), 2 * ks + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+      mma_f16(kk[0], a, b[0], b[1]);
+      mma_f16(kk[1], a, b[2], b[3]);
+      mma_f16(qk[0], c, b[0], b[1]);
+      mma_f16(qk[1], c, b[2], b[3]);
     }
-    uint32_t b[8][4];  // both k-steps
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < tiles)
-        ldsm_x4(sm + Geo::kK + tile_at<kPieces>(8 * j + (lane & 7), 2 * ks + (lane >> 3)), b[j][0], b[j][1], b[j][2], b[j][3]);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < tiles) {
-          mma_f16(kk[j], a[x], b[j][2 * x], b[j][2 * x + 1]);
-          mma_f16(qk[j], c[x], b[j][2 * x], b[j][2 * x + 1]);
-        }
-  }
-  const int y0 = 16 * warp + g;
-  const float yh[2] = {Ghi[y0], Ghi[y0 + 8]}, yl[2] = {Glo[y0], Glo[y0 + 8]};
-  const float yb[2] = {E[kBeta * kC + y0] * E[kKappa * kC + y0], E[kBeta * kC + y0 + 8] * E[kKappa * kC + y0 + 8]};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int x = 8 * j + 2 * t;
-    const float2 xh = *reinterpret_cast<const float2*>(Ghi + x), xl = *reinterpret_cast<const float2*>(Glo + x);
-    const float2 xk = *reinterpret_cast<const float2*>(E + kKappa * kC + x);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int y = y0 + 8 * r;
-      float a[2] = {0.f, 0.f}, c[2] = {0.f, 0.f};
-      if (j < tiles) {
-        const float d0 = exp2_fast((yh[r] - xh.x) + (yl[r] - xl.x)), d1 = exp2_fast((yh[r] - xh.y) + (yl[r] - xl.y));
-        a[0] = x < y ? yb[r] * xk.x * (kk[j][2 * r] * d0) : 0.f;
-        a[1] = x + 1 < y ? yb[r] * xk.y * (kk[j][2 * r + 1] * d1) : 0.f;
-        c[0] = x <= y ? qk[j][2 * r] * d0 : 0.f;
-        c[1] = x + 1 <= y ? qk[j][2 * r + 1] * d1 : 0.f;
+      const int y = 16 * bi + g + 8 * r;
+      const float yh = Ghi[y], yl = Glo[y], yb = E[kBeta * kC + y] * E[kKappa * kC + y];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int x = 16 * bj + 8 * j + 2 * t;
+        const float2 xh = *reinterpret_cast<const float2*>(Ghi + x), xl = *reinterpret_cast<const float2*>(Glo + x);
+        const float2 xk = *reinterpret_cast<const float2*>(E + kKappa * kC + x);
+        const float d0 = exp2_fast((yh - xh.x) + (yl - xl.x)), d1 = exp2_fast((yh - xh.y) + (yl - xl.y));
+        *reinterpret_cast<float2*>(A + y * kLd + x) = make_float2(x < y ? yb * xk.x * (kk[j][2 * r] * d0) : 0.f,
+                                                                  x + 1 < y ? yb * xk.y * (kk[j][2 * r + 1] * d1) : 0.f);
+        *reinterpret_cast<uint32_t*>(buf + Geo::kP + tile_at(y, 2 * bj + j) + 4 * t) =
+            pack_half(x <= y ? qk[j][2 * r] * d0 : 0.f, x + 1 <= y ? qk[j][2 * r + 1] * d1 : 0.f);
       }
-      *reinterpret_cast<float2*>(A + y * kLd + x) = make_float2(a[0], a[1]);
-      *reinterpret_cast<uint32_t*>(buf + Geo::kP + tile_at<8>(y, j) + 4 * t) = pack_half(c[0], c[1]);
     }
+  }
+  // what the products of blocks read above the diagonal
+  if ((warp & 1) == 0) {
+    float* z = A + (16 * warp + (lane >> 1)) * kLd + 16 * (warp + 1) + 8 * (lane & 1);
+    *reinterpret_cast<float4*>(z) = *reinterpret_cast<float4*>(z + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncwarp();
 
@@ -371,7 +354,13 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     for (int i = 0; i < 16; ++i) {
       float s = i == c ? 1.f : 0.f;
 #pragma unroll
-      for (int l = 0; l < i; ++l) s -= D[i * kLd + l] * x[l];
+      for (int l = 0; l < i; l += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(D + i * kLd + l);
+        s -= d.x * x[l];
+        if (l + 1 < i) s -= d.y * x[l + 1];
+        if (l + 2 < i) s -= d.z * x[l + 2];
+        if (l + 3 < i) s -= d.w * x[l + 3];
+      }
       x[i] = s;
     }
     __syncwarp();
@@ -380,7 +369,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       for (int i = 0; i < 16; ++i) D[i * kLd + c] = x[i];
     }
   }
-  bar_sync(5, 128);
+  bar_sync(barrier, 128);
   // Blocks of 32, then 64: the lower left of the inverse is -T22 (A21 T11).
   float* M = reinterpret_cast<float*>(smem + Geo::kTmp);
   {
@@ -402,9 +391,9 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       return make_float4(sign * s[0], sign * s[1], sign * s[2], sign * s[3]);
     };
     *reinterpret_cast<float4*>(H + y * 20 + x) = product(D + (16 + y) * kLd, D, kLd, 1.f);
-    bar_sync(5, 128);
+    bar_sync(barrier, 128);
     *reinterpret_cast<float4*>(D + (16 + y) * kLd + x) = product(D + (16 + y) * kLd + 16, H, 20, -1.f);
-    bar_sync(5, 128);
+    bar_sync(barrier, 128);
   }
   {
     const int y = (tid >> 3) * 2, x = (tid & 7) * 4;  // two rows and 4 columns
@@ -413,7 +402,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int l = 0; l < 32; l += 4) {
         const float4 u = *reinterpret_cast<const float4*>(left + l), w = *reinterpret_cast<const float4*>(left + kLd + l);
         const float a[4] = {u.x, u.y, u.z, u.w}, c[4] = {w.x, w.y, w.z, w.w};
@@ -429,15 +418,15 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     product(A + (32 + y) * kLd, A, kLd, s);
 #pragma unroll
     for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(M + (y + r) * 36 + x) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
-    bar_sync(5, 128);
+    bar_sync(barrier, 128);
     product(A + (32 + y) * kLd + 32, M, 36, s);
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       *reinterpret_cast<float4*>(A + (32 + y + r) * kLd + x) = make_float4(-s[r][0], -s[r][1], -s[r][2], -s[r][3]);
-    bar_sync(5, 128);
+    bar_sync(barrier, 128);
   }
   // T in two parts; zeros above the diagonal
-#pragma unroll
+#pragma unroll 1
   for (int i = tid; i < kC * 8; i += 128) {
     const int y = i >> 3, c = i & 7;
     const float4 u = *reinterpret_cast<const float4*>(A + y * kLd + 8 * c), w = *reinterpret_cast<const float4*>(A + y * kLd + 8 * c + 4);
@@ -448,226 +437,327 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       const int x = 8 * c + 2 * e;
       split2(x <= y ? a[2 * e] : 0.f, x + 1 <= y ? a[2 * e + 1] : 0.f, hi[e], lo[e]);
     }
-    const int at = tile_at<8>(y, c);
+    const int at = tile_at(y, c);
     *reinterpret_cast<uint4*>(buf + Geo::kT + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(buf + Geo::kT + kC * kC * 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(ChunkGeo<DK, DV>::kThreads, 1) delta_chunks_kernel(const DeltaParams p) {
-  using Geo = ChunkGeo<DK, DV>;
-  extern __shared__ __align__(128) uint8_t smem[];
+// Waits of a warp.  After one that runs out nothing waits on any; the others' run out too.
+__device__ __forceinline__ bool warp_wait(const DeltaParams& p, uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, wait_for(bar, parity));
+  if (!ok && (threadIdx.x & 31) == 0) raise(p.status, HYB_STATUS_TIMEOUT);
+  return ok;
+}
+
+template <int DK>
+__device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem, uint64_t* bars, uint32_t tmem, const Run& run, int hv,
+                                            int chunks, int tid) {
+  using Geo = ChunkGeo<DK>;
+  constexpr int kKeys = DK / 2;  // of the state, a thread's; its tokens: kC / 2
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, h = warp >> 2, row = 32 * (warp & 3) + lane;
+  const uint32_t sm = smem_u32(smem), mine = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  float* most_s = reinterpret_cast<float*>(smem + Geo::kMost);
+  float* most_w = most_s + 256;
+  const bool there = row < p.DV;
+  float* state = p.state + (((int64_t)run.slot * p.Hv + hv) * DK + h * kKeys) * p.DV + row;
+  // two lanes' channels of every other token: rows of 4 bytes; keep() and swap() turn them into a channel's tokens
+  const int odd = lane & 1;
+  const uint16_t* v0 = p.v + (int64_t)(run.t0 + 32 * h + odd) * p.v_stride + (int64_t)hv * p.DV + (row & ~1);
+  uint16_t* out0 = p.out + (int64_t)(run.t0 + 32 * h + odd) * p.out_stride + (int64_t)hv * p.DV + (row & ~1);
+  auto swap = [&](uint32_t w) {  // (channel, its neighbour) of a token <-> (token, the next) of a channel
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w << 16 : w, 1);  // the upper half: what the neighbour needs
+    return odd ? (got >> 16) | (w & 0xffff0000u) : (w & 0xffffu) | (got & 0xffff0000u);
+  };
+  bool alive = true, ok = true;
+  float unit = 1.f, sig = 1.f, om = 1.f;
+  const uint32_t my_s = mine + kColS + h * kKeys;
+#pragma unroll 1
+  for (int i = 0; i < kKeys; i += 32) {
+    uint32_t r[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[e] = there ? __float_as_uint(state[(int64_t)(i + e) * p.DV]) : 0u;
+    tmem_store32(my_s + i, r);
+  }
+  tmem_wait_store();
+
+  // The outputs of chunk c: 32 tokens of this thread's channel.
+  auto outputs = [&](int c) {
+    const float* E = reinterpret_cast<const float*>(smem + (c % 3) * Geo::kBytes + Geo::kE) + 32 * h;
+    const int n = there && alive ? run.n - c * kC - 32 * h - odd : 0;
+    uint16_t* out = out0 + (int64_t)(c * kC) * p.out_stride;
+    const int64_t step = 2 * p.out_stride;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 16) {
+      uint32_t q[16], u[16];
+      tmem_load16(mine + kColQ + 32 * h + i0, q);
+      tmem_load16(mine + kColP + 32 * h + i0, u);
+      tmem_wait_load();
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(E + kDecay * kC + i0 + i), o = *reinterpret_cast<const float4*>(E + kOut * kC + i0 + i);
+        const float dd[4] = {d.x, d.y, d.z, d.w}, oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          u[i + e] = __float_as_uint((__uint_as_float(q[i + e]) * dd[e] + __uint_as_float(u[i + e]) * om) * (oo[e] * sig));
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i += 2, out += step) {
+        const uint32_t w = swap(pack_bf16(__uint_as_float(u[i]), __uint_as_float(u[i + 1])));
+        if (i0 + i < n) *reinterpret_cast<uint32_t*>(out) = w;
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && alive) mbar_arrive(bars + kFree + c % 3);
+  };
+
+#pragma unroll 1
+  for (int c = 0;; ++c) {
+    const int place = c % 3;
+    if (c > 0) {
+      alive = alive && warp_wait(p, bars + kDoneS, (c - 1) & 1);
+      fence_after();
+    }
+    float s = 1.f;
+    uint32_t v[16];
+    const uint64_t operand = matrix_at(sm + place * Geo::kBytes, 16), across = matrix_at(sm + place * Geo::kBytes, 8192);
+    if (c < chunks) {
+    // sigma: the largest element of the column goes to [2^6, 2^7)
+    float top = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < kKeys; i += 32) {
+      uint32_t r[32];
+      tmem_load(my_s + i, r);
+      tmem_wait_load();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(r[e])));
+    }
+    most_s[128 * h + row] = top;
+    bar_sync(2, 256);
+    top = fmaxf(top, most_s[128 * (1 - h) + row]);
+    s = pow2_of(field_of(top * unit, 127 - 30, 127 + 110) - 6);
+    {
+      const float f = fminf(unit / s, FLT_MAX);
+#pragma unroll 1
+      for (int i = 0; i < kKeys; i += 32) {
+        uint32_t r[32], hi[16], lo[16];
+        tmem_load(my_s + i, r);
+        tmem_wait_load();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) split2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f, hi[e], lo[e]);
+        tmem_store16(mine + kColSh + (h * kKeys + i) / 2, hi);
+        tmem_store16(mine + kColSl + (h * kKeys + i) / 2, lo);
+      }
+    }
+    {
+      const int n = there ? run.n - c * kC - 32 * h - odd : 0;
+      const uint16_t* from = v0 + (int64_t)(c * kC) * p.v_stride;
+      const int64_t step = 2 * p.v_stride;
+#pragma unroll
+      for (int i = 0; i < 16; ++i, from += step) v[i] = 2 * i < n ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+    }
+    tmem_wait_store();
+    fence_before();
+    bar_sync(2, 256);
+    if (warp == 0 && ok) {
+      fence_after();
+      ok = warp_wait(p, bars + kFull + place, (c / 3) & 1);
+      if (ok && elect_one()) {
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k)
+          mma_tmem_on(tmem + kColX, tmem + kColSh + 8 * k, operand, Geo::kK + (k / 4) * 8192 + (k % 4) * 32, product_of(kC, false), k > 0);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k)
+          mma_tmem_on(tmem + kColX, tmem + kColSl + 8 * k, operand, Geo::kK + (k / 4) * 8192 + (k % 4) * 32, product_of(kC, false), true);
+        commit_to(bars + kDoneX);
+      }
+    }
+    __syncwarp();
+    }
+    if (c > 0) outputs(c - 1);
+    if (c == chunks) break;
+    sig = s;
+    const float* E = reinterpret_cast<const float*>(smem + place * Geo::kBytes + Geo::kE) + 32 * h;
+    alive = alive && warp_wait(p, bars + kFull + place, (c / 3) & 1);
+    alive = alive && warp_wait(p, bars + kDoneX, c & 1);
+    fence_after();
+    // W = diag(beta) (V - diag(e^G) X), and its omega
+    uint32_t x[32];
+    tmem_load(mine + kColX + 32 * h, x);
+    tmem_wait_load();
+    const float inv = 1.f / sig;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(E + kForget * kC + i), w = *reinterpret_cast<const float4*>(E + kBeta * kC + i);
+      const float ff[4] = {f.x, f.y, f.z, f.w}, ww[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t vv[2] = {swap(v[i / 2]), swap(v[i / 2 + 1])};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = (e & 1 ? bf16_hi(vv[e / 2]) : bf16_lo(vv[e / 2])) * inv * ww[e] - __uint_as_float(x[i + e]) * ff[e];
+        x[i + e] = __float_as_uint(y);
+        most = fmaxf(most, fabsf(y));
+      }
+    }
+    most_w[128 * h + row] = most;
+    bar_sync(2, 256);
+    most = fmaxf(most, most_w[128 * (1 - h) + row]);
+    om = pow2_of(field_of(most, 127 - 60, 127 + 96) - 6);
+    const float back = 1.f / om;
+    {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) split2(__uint_as_float(x[2 * i]) * back, __uint_as_float(x[2 * i + 1]) * back, hi[i], lo[i]);
+      tmem_store16(mine + kColW + 16 * h, hi);
+      tmem_store16(mine + kColW + 32 + 16 * h, lo);
+    }
+    tmem_wait_store();
+    fence_before();
+    bar_sync(2, 256);
+    if (warp == 0 && ok && elect_one()) {
+      fence_after();
+      // U^T = W^T T^T over the place of X: tokens 16 k .. take part in those from 16 k on
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_tmem_on(tmem + kColX + 16 * k, tmem + kColW + (part == 1 ? 32 : 0) + 8 * k,
+                   operand, Geo::kT + (part == 2 ? kC * kC * 2 : 0) + 2048 * k + 32 * k, product_of(kC - 16 * k, false),
+                   part > 0 || k > 0);
+      commit_to(bars + kDoneU);
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k)
+        mma_tmem_on(tmem + kColQ, tmem + kColSh + 8 * k, operand, Geo::kQ + (k / 4) * 8192 + (k % 4) * 32, product_of(kC, false), k > 0);
+    }
+    __syncwarp();
+    // The state's new unit is the larger of its decayed part's and of U's; meanwhile it decays.
+    const float whole = E[kWhole * kC - 32 * h];
+    const float now = fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om);
+    {
+      const float f = whole * fminf(unit / now, FLT_MAX);
+#pragma unroll 1
+      for (int i = 0; i < kKeys; i += 32) {
+        uint32_t r[32];
+        tmem_load(my_s + i, r);
+        tmem_wait_load();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+        tmem_store32(my_s + i, r);
+      }
+    }
+    unit = now;
+    alive = alive && warp_wait(p, bars + kDoneU, c & 1);
+    fence_after();
+    tmem_load(mine + kColX + 32 * h, x);
+    tmem_wait_load();
+    {
+      const float part = sig * om / now;
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(E + kKappa * kC + i);
+        x[i] = __float_as_uint(__uint_as_float(x[i]) * k.x), x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * k.y);
+        x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * k.z), x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * k.w);
+        hi[i / 2] = pack_half(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        hi[i / 2 + 1] = pack_half(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+      }
+      tmem_store16(mine + kColSl + 16 * h, hi);  // its part of the outputs, in place of the state's lower halves
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(E + kLeft * kC + i);
+        split2(__uint_as_float(x[i]) * (l.x * part), __uint_as_float(x[i + 1]) * (l.y * part), hi[i / 2], lo[i / 2]);
+        split2(__uint_as_float(x[i + 2]) * (l.z * part), __uint_as_float(x[i + 3]) * (l.w * part), hi[i / 2 + 1], lo[i / 2 + 1]);
+      }
+      tmem_store16(mine + kColW + 16 * h, hi);
+      tmem_store16(mine + kColW + 32 + 16 * h, lo);
+    }
+    tmem_wait_store();
+    fence_before();
+    bar_sync(2, 256);
+    if (warp == 0 && ok && elect_one()) {
+      fence_after();
+      // P U, and S^T += U^T K
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_tmem_on(tmem + kColP + 16 * k, tmem + kColSl + 8 * k, operand, Geo::kP + 2048 * k + 32 * k, product_of(kC - 16 * k, false), k > 0);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_tmem_on(tmem + kColS, tmem + kColW + 32 * part + 8 * k, across, Geo::kK + 2048 * k, product_of(DK, true), true);
+      commit_to(bars + kDoneS);
+    }
+    __syncwarp();
+  }
+#pragma unroll 1
+  for (int i = 0; i < kKeys; i += 32) {
+    uint32_t r[32];
+    tmem_load(my_s + i, r);
+    tmem_wait_load();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (there && alive) state[(int64_t)(i + e) * p.DV] = __uint_as_float(r[e]) * unit;
+  }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kChunkThreads, 1) delta_chunks_kernel(const DeltaParams p) {
+  using Geo = ChunkGeo<DK>;
+  extern __shared__ uint8_t raw[];
   pdl_wait_primary();
   pdl_allow_dependents();
   const int b = blockIdx.x / p.Hv, hv = blockIdx.x % p.Hv, hk = hv / (p.Hv / p.Hk);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const Run run = read_run(p, b, hv == 0 && tid == 0);
   if (run.n <= 0) return;
   const int chunks = (run.n + kC - 1) / kC;
-
-  // barriers 1, 2: a buffer is full; 3, 4: it is free again; 5: the preparing warps' own
-  if (warp >= Geo::kScan) {
-    for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) bar_sync(3 + (c & 1), Geo::kThreads);
-      chunk_prepare<DK, DV>(p, smem, smem + (c & 1) * Geo::kBytes, run.t0 + c * kC, min(run.n - c * kC, kC),
-                            min(max(run.n - (c + 1) * kC, 0), kC), hk, hv, tid - Geo::kScan * 32);
-      __threadfence_block();
-      bar_arrive(1 + (c & 1), Geo::kThreads);
-      if (c + 1 < chunks) bar_sync(5, 128);  // A is read no more
-    }
-    return;
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo::kBars);
+  uint32_t* where = reinterpret_cast<uint32_t*>(smem + Geo::kTmem);
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(bars + kFull + i, 4), mbar_init(bars + kFree + i, 8);
+    mbar_init(bars + kDoneX, 1);
+    mbar_init(bars + kDoneU, 1);
+    mbar_init(bars + kDoneS, 1);
+    fence_mbar_init();
   }
-
-  // The warp's 16 columns of the state, transposed and divided by unit[]: rows (columns of S) g and g + 8, keys
-  // 8 j + 2 t and the next.
-  const int dv0 = 16 * warp;
-  float* state = p.state + ((int64_t)run.slot * p.Hv + hv) * DK * DV + dv0;
-  float S[DK / 8][4], unit[2] = {1.f, 1.f};
-#pragma unroll
-  for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[j][e] = state[(int64_t)(8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)];
-
-  for (int c = 0; c < chunks; ++c) {
-    uint8_t* buf = smem + (c & 1) * Geo::kBytes;
-    const uint32_t sm = smem_u32(buf);
-    const float* E = reinterpret_cast<const float*>(buf + Geo::kE) + 2 * t;  // this lane's tokens: + 8 j
-    constexpr int kPieces = DK / 8;
-    // sigma: the largest element of each column goes to [2^6, 2^7)
-    float sig[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = 0.f;
-#pragma unroll
-      for (int j = 0; j < DK / 8; ++j) top = fmaxf(top, fmaxf(fabsf(S[j][2 * r]), fabsf(S[j][2 * r + 1])));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      sig[r] = pow2_of(field_of(top * unit[r], 127 - 30, 127 + 110) - 6);
-      const float f = unit[r] / sig[r];
-#pragma unroll
-      for (int j = 0; j < DK / 8; ++j) S[j][2 * r] *= f, S[j][2 * r + 1] *= f;
-    }
-    bar_sync(1 + (c & 1), Geo::kThreads);
-    float X[8][4];  // 8 tiles of 8 tokens
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) X[j][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t hi[4], lo[4];
-      split_a(S[2 * ks], S[2 * ks + 1], hi, lo);
-      uint32_t x[4][4];  // two token tiles each
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        ldsm_x4(sm + Geo::kK + tile_at<kPieces>(16 * j + (lane & 7) + 8 * (lane >> 4), 2 * ks + ((lane >> 3) & 1)), x[j][0], x[j][1],
-                x[j][2], x[j][3]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mma_f16(X[j], hi, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mma_f16(X[j], lo, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-    }
-    // W^T = (V^T - X^T diag(e^G)) diag(beta), and its omega
-    const float inv[2] = {1.f / sig[0], 1.f / sig[1]};
-    float most[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint32_t v[4];  // tokens 8 j .., columns g; columns g + 8; the next tile's
-      ldsm_x4_t(sm + Geo::kV + tile_at<DV / 8>(8 * j + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)), v[0], v[1], v[2],
-                v[3]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 f = *reinterpret_cast<const float2*>(E + kForget * kC + 8 * (j + e));
-        const float2 w = *reinterpret_cast<const float2*>(E + kBeta * kC + 8 * (j + e));
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          X[j + e][2 * r] = bf16_lo(v[2 * e + r]) * inv[r] * w.x - X[j + e][2 * r] * f.x;
-          X[j + e][2 * r + 1] = bf16_hi(v[2 * e + r]) * inv[r] * w.y - X[j + e][2 * r + 1] * f.y;
-          most[r] = fmaxf(most[r], fmaxf(fabsf(X[j + e][2 * r]), fabsf(X[j + e][2 * r + 1])));
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(where)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *where;
+  if (warp < 8) {
+    scan_chunks<DK>(p, smem, bars, tmem, run, hv, chunks, tid);
+  } else {
+    const int group = (warp - 8) >> 2, me = tid & 127;
+    int* go = reinterpret_cast<int*>(smem + Geo::kTmem + 4 + 4 * group);
+#pragma unroll 1
+    for (int c = group; c < chunks; c += 2) {
+      const int place = c % 3, next = c + 2;
+      if (c >= 3) {
+        if (me == 0) {
+          const bool ok = wait_for(bars + kFree + place, (c / 3 - 1) & 1);
+          if (!ok) raise(p.status, HYB_STATUS_TIMEOUT);
+          *go = ok;
         }
+        bar_sync(3 + group, 128);
+        if (*go == 0) break;
       }
-    }
-    float om[2], back[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
-      most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
-      om[r] = pow2_of(field_of(most[r], 127 - 60, 127 + 96) - 6);
-      back[r] = 1.f / om[r];
-    }
-    // U^T = W^T T^T: T is lower triangular, so tokens 8 j .. take k-steps up to j / 2
-    float U[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[j][e] = 0.f, X[j][e] *= back[e >> 1];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t hi[4], lo[4];
-      split_a(X[2 * ks], X[2 * ks + 1], hi, lo);
-      auto tiles = [&](int part, const uint32_t (&a)[4], const uint32_t (&c)[4], bool both) {
-        uint32_t x[4][4];
-#pragma unroll
-        for (int j = ks; j < 4; ++j)
-          ldsm_x4(sm + part + tile_at<8>(16 * j + (lane & 7) + 8 * (lane >> 4), 2 * ks + ((lane >> 3) & 1)), x[j][0], x[j][1], x[j][2],
-                  x[j][3]);
-#pragma unroll
-        for (int j = 2 * ks; j < 8; ++j) mma_f16(U[j], a, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-        if (!both) return;
-#pragma unroll
-        for (int j = 2 * ks; j < 8; ++j) mma_f16(U[j], c, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-      };
-      tiles(Geo::kT, hi, lo, true);
-      tiles(Geo::kT + kC * kC * 2, hi, hi, false);
-    }
-    // O^T = S^T Q^T diag(e^G) + U^T P^T, and S^T = e^G_C S^T + U^T diag(kappa e^(G_C - G)) K, in units of sigma omega
-    float O[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) O[j][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      const uint32_t hi[4] = {pack_half(S[2 * ks][0], S[2 * ks][1]), pack_half(S[2 * ks][2], S[2 * ks][3]),
-                              pack_half(S[2 * ks + 1][0], S[2 * ks + 1][1]), pack_half(S[2 * ks + 1][2], S[2 * ks + 1][3])};
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        uint32_t x[4];
-        ldsm_x4(sm + Geo::kQ + tile_at<kPieces>(8 * j + (lane & 7) + 8 * (lane >> 4), 2 * ks + ((lane >> 3) & 1)), x[0], x[1], x[2],
-                x[3]);
-        mma_f16(O[j], hi, x[0], x[1]);
-        mma_f16(O[j + 1], hi, x[2], x[3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 d = *reinterpret_cast<const float2*>(E + kDecay * kC + 8 * j);
-      const float2 k = *reinterpret_cast<const float2*>(E + kKappa * kC + 8 * j);
-      O[j][0] *= d.x * back[0], O[j][1] *= d.y * back[0], O[j][2] *= d.x * back[1], O[j][3] *= d.y * back[1];
-      U[j][0] *= k.x, U[j][1] *= k.y, U[j][2] *= k.x, U[j][3] *= k.y;
-    }
-    const float whole = E[kWhole * kC - 2 * t];
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[j][e] *= whole * back[e >> 1];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const uint32_t u[4] = {pack_half(U[2 * ks][0], U[2 * ks][1]), pack_half(U[2 * ks][2], U[2 * ks][3]),
-                             pack_half(U[2 * ks + 1][0], U[2 * ks + 1][1]), pack_half(U[2 * ks + 1][2], U[2 * ks + 1][3])};
-#pragma unroll
-      for (int j = 2 * ks; j < 8; j += 2) {
-        uint32_t x[4];
-        ldsm_x4(sm + Geo::kP + tile_at<8>(8 * j + (lane & 7) + 8 * (lane >> 4), 2 * ks + ((lane >> 3) & 1)), x[0], x[1], x[2], x[3]);
-        mma_f16(O[j], u, x[0], x[1]);
-        mma_f16(O[j + 1], u, x[2], x[3]);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 l = *reinterpret_cast<const float2*>(E + kLeft * kC + 8 * (2 * ks + e));
-        U[2 * ks + e][0] *= l.x, U[2 * ks + e][1] *= l.y, U[2 * ks + e][2] *= l.x, U[2 * ks + e][3] *= l.y;
-      }
-      uint32_t hi[4], lo[4];
-      split_a(U[2 * ks], U[2 * ks + 1], hi, lo);
-#pragma unroll
-      for (int part = 0; part < DK / 8; part += 8) {
-        uint32_t x[4][4];  // K as [token][key]: tokens 16 ks .., keys 8 j .. and the next 8
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ldsm_x4_t(sm + Geo::kK + tile_at<kPieces>(16 * ks + (lane & 15), part + 2 * j + (lane >> 4)), x[j][0], x[j][1], x[j][2],
-                    x[j][3]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mma_f16(S[part + j], hi, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mma_f16(S[part + j], lo, x[j / 2][2 * (j & 1)], x[j / 2][2 * (j & 1) + 1]);
-      }
-    }
-    unit[0] = sig[0] * om[0], unit[1] = sig[1] * om[1];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 s = *reinterpret_cast<const float2*>(E + kOut * kC + 8 * j);
-      O[j][0] *= s.x * unit[0], O[j][1] *= s.y * unit[0], O[j][2] *= s.x * unit[1], O[j][3] *= s.y * unit[1];
-    }
-    if (c + 2 < chunks) bar_arrive(3 + (c & 1), Geo::kThreads);
-    // the outputs, back in token order
-    const int n = min(run.n - c * kC, kC);
-    uint16_t* out = p.out + (int64_t)(run.t0 + c * kC) * p.out_stride + (int64_t)hv * DV + dv0 + 2 * t;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t a = transpose8(pack_bf16(O[j][0], O[j][1])), d = transpose8(pack_bf16(O[j][2], O[j][3]));
-      if (8 * j + g < n) {
-        uint16_t* to = out + (int64_t)(8 * j + g) * p.out_stride;
-        *reinterpret_cast<uint32_t*>(to) = a;
-        *reinterpret_cast<uint32_t*>(to + 8) = d;
-      }
+      chunk_prepare<DK>(p, smem + Geo::kWork + group * Geo::kWorkBytes, smem + place * Geo::kBytes, 3 + group, run.t0 + c * kC,
+                        min(run.n - c * kC, kC), run.t0 + next * kC, min(max(run.n - next * kC, 0), kC), hk, hv, me);
+      fence_smem();
+      __syncwarp();
+      if ((me & 31) == 0) mbar_arrive(bars + kFull + place);
+      bar_sync(3 + group, 128);  // A is read no more
     }
   }
-#pragma unroll
-  for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      state[(int64_t)(8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] = S[j][e] * unit[e >> 1];
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 cudaError_t launch(void (*f)(DeltaParams), int blocks, int threads, int smem, const DeltaParams& p, cudaStream_t s) {
@@ -688,11 +778,6 @@ cudaError_t launch(void (*f)(DeltaParams), int blocks, int threads, int smem, co
   return cudaLaunchKernelEx(&c, f, p);
 }
 
-template <int DK, int DV>
-cudaError_t chunks(const DeltaParams& p, cudaStream_t s) {
-  return launch(delta_chunks_kernel<DK, DV>, p.B * p.Hv, ChunkGeo<DK, DV>::kThreads, ChunkGeo<DK, DV>::kTotal, p, s);
-}
-
 }  // namespace
 
 cudaError_t launch_delta_steps(const DeltaParams& p, cudaStream_t s) {
@@ -700,8 +785,8 @@ cudaError_t launch_delta_steps(const DeltaParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_delta_chunks(const DeltaParams& p, cudaStream_t s) {
-  if (p.DK == 128) return p.DV == 128 ? chunks<128, 128>(p, s) : chunks<128, 64>(p, s);
-  return p.DV == 128 ? chunks<64, 128>(p, s) : chunks<64, 64>(p, s);
+  if (p.DK == 128) return launch(delta_chunks_kernel<128>, p.B * p.Hv, kChunkThreads, ChunkGeo<128>::kTotal, p, s);
+  return launch(delta_chunks_kernel<64>, p.B * p.Hv, kChunkThreads, ChunkGeo<64>::kTotal, p, s);
 }
 
 }  // namespace hyb

@@ -159,7 +159,7 @@ struct ChunkGeo {
 enum { kFull, kFree = 3, kDoneX = 6, kDoneU, kDoneS };
 // Columns of the tensor memory: S^T; as f16, upper and lower halves; X^T, then U^T; Q S; W or U in two parts; P U
 enum { kColS = 0, kColSh = 128, kColSl = 192, kColX = 256, kColQ = 320, kColW = 384, kColP = 448 };
-// The factors' rows: e^G; beta e^G kappa; beta; kappa; e^(G_C - G); scale kappa of q; e^G_C
+// The factors' rows: e^G times that of q; -beta e^G kappa; beta; kappa; e^(G_C - G); scale kappa of q; e^G_C
 enum { kDecay, kForget, kBeta, kKappa, kLeft, kOut, kWhole };
 
 // Byte offset of 16-byte piece c of row r in tiles of 64 rows of 8 pieces, moved so that 8 rows' pieces of one column lie
@@ -178,11 +178,13 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 // Two fp32 as two f16 parts.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_half(x, y);
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  lo = pack_half(x - b.x, y - b.y);
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_half(x.x, x.y);
+  x = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi)), make_float2(-1.f, -1.f), x);
+  lo = pack_half(x.x, x.y);
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -211,16 +213,19 @@ __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, f
   for (int i = 0; i < 4; ++i) {
     const int at = tid + 128 * (first + i), r = at / kPieces, c = at % kPieces;
     const uint32_t z[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t both = 0;  // magnitudes of bf16 order as integers
+    uint32_t top = 0;  // magnitudes of bf16 order as integers
 #pragma unroll
-    for (int e = 0; e < 4; ++e) both = __vmaxu2(both, z[e] & 0x7fff7fffu);
+    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, z[e] & 0x7fff7fffu);
 #pragma unroll
-    for (int o = 1; o < kPieces; o <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
-    const uint32_t e = min(max(max(both & 0xffffu, both >> 16) >> 7, 1u), 253u);
-    const float inv = pow2_of(254u - e);
+    for (int o = 1; o < kPieces; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t e = min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u);
+    const float2 inv = both(pow2_of(254u - e));
     uint32_t y[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) y[x] = pack_half(bf16_lo(z[x]) * inv, bf16_hi(z[x]) * inv);
+    for (int x = 0; x < 4; ++x) {
+      const float2 w = mul2(make_float2(bf16_lo(z[x]), bf16_hi(z[x])), inv);
+      y[x] = pack_half(w.x, w.y);
+    }
     *reinterpret_cast<uint4*>(tile + tile_at(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
     if (c == 0) kappa[r] = pow2_of(e);
   }
@@ -294,8 +299,10 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = r0 + x;
-      E[kForget * kC + r] = (x ? b1 : b0) * E[kDecay * kC + r] * E[kKappa * kC + r];
-      E[kOut * kC + r] = p.scale * kq[r];
+      const float decay = E[kDecay * kC + r], out = p.scale * kq[r];
+      E[kForget * kC + r] = -(x ? b1 : b0) * decay * E[kKappa * kC + r];
+      E[kOut * kC + r] = out;
+      E[kDecay * kC + r] = decay * out;
     }
   }
 
@@ -397,11 +404,8 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
   }
   {
     const int y = (tid >> 3) * 2, x = (tid & 7) * 4;  // two rows and 4 columns
-    auto product = [&](const float* left, const float* right, int ld, float (&s)[2][4]) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
+    auto product = [&](const float* left, const float* right, int ld, float2 (&s)[2][2]) {
+      s[0][0] = s[0][1] = s[1][0] = s[1][1] = both(0.f);
 #pragma unroll 1
       for (int l = 0; l < 32; l += 4) {
         const float4 u = *reinterpret_cast<const float4*>(left + l), w = *reinterpret_cast<const float4*>(left + kLd + l);
@@ -409,20 +413,21 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 b = *reinterpret_cast<const float4*>(right + (l + i) * ld + x);
-          s[0][0] += a[i] * b.x, s[0][1] += a[i] * b.y, s[0][2] += a[i] * b.z, s[0][3] += a[i] * b.w;
-          s[1][0] += c[i] * b.x, s[1][1] += c[i] * b.y, s[1][2] += c[i] * b.z, s[1][3] += c[i] * b.w;
+          const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
+          s[0][0] = fma2(both(a[i]), b0, s[0][0]), s[0][1] = fma2(both(a[i]), b1, s[0][1]);
+          s[1][0] = fma2(both(c[i]), b0, s[1][0]), s[1][1] = fma2(both(c[i]), b1, s[1][1]);
         }
       }
     };
-    float s[2][4];
+    float2 s[2][2];
     product(A + (32 + y) * kLd, A, kLd, s);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(M + (y + r) * 36 + x) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+    for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(M + (y + r) * 36 + x) = make_float4(s[r][0].x, s[r][0].y, s[r][1].x, s[r][1].y);
     bar_sync(barrier, 128);
     product(A + (32 + y) * kLd + 32, M, 36, s);
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-      *reinterpret_cast<float4*>(A + (32 + y + r) * kLd + x) = make_float4(-s[r][0], -s[r][1], -s[r][2], -s[r][3]);
+      *reinterpret_cast<float4*>(A + (32 + y + r) * kLd + x) = make_float4(-s[r][0].x, -s[r][0].y, -s[r][1].x, -s[r][1].y);
     bar_sync(barrier, 128);
   }
   // T in two parts; zeros above the diagonal
@@ -435,7 +440,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int x = 8 * c + 2 * e;
-      split2(x <= y ? a[2 * e] : 0.f, x + 1 <= y ? a[2 * e + 1] : 0.f, hi[e], lo[e]);
+      split2(make_float2(x <= y ? a[2 * e] : 0.f, x + 1 <= y ? a[2 * e + 1] : 0.f), hi[e], lo[e]);
     }
     const int at = tile_at(y, c);
     *reinterpret_cast<uint4*>(buf + Geo::kT + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -461,13 +466,13 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
   float* most_w = most_s + 256;
   const bool there = row < p.DV;
   float* state = p.state + (((int64_t)run.slot * p.Hv + hv) * DK + h * kKeys) * p.DV + row;
-  // two lanes' channels of every other token: rows of 4 bytes; keep() and swap() turn them into a channel's tokens
+  // two lanes' channels of every other token: words that swap() turns into a channel's two tokens
   const int odd = lane & 1;
   const uint16_t* v0 = p.v + (int64_t)(run.t0 + 32 * h + odd) * p.v_stride + (int64_t)hv * p.DV + (row & ~1);
   uint16_t* out0 = p.out + (int64_t)(run.t0 + 32 * h + odd) * p.out_stride + (int64_t)hv * p.DV + (row & ~1);
+  const uint32_t halves = odd ? 0x3276u : 0x5410u;
   auto swap = [&](uint32_t w) {  // (channel, its neighbour) of a token <-> (token, the next) of a channel
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w << 16 : w, 1);  // the upper half: what the neighbour needs
-    return odd ? (got >> 16) | (w & 0xffff0000u) : (w & 0xffffu) | (got & 0xffff0000u);
+    return __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), halves);
   };
   bool alive = true, ok = true;
   float unit = 1.f, sig = 1.f, om = 1.f;
@@ -496,14 +501,17 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 d = *reinterpret_cast<const float4*>(E + kDecay * kC + i0 + i), o = *reinterpret_cast<const float4*>(E + kOut * kC + i0 + i);
-        const float dd[4] = {d.x, d.y, d.z, d.w}, oo[4] = {o.x, o.y, o.z, o.w};
+        const float2 dd[2] = {make_float2(d.x, d.y), make_float2(d.z, d.w)}, oo[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          u[i + e] = __float_as_uint((__uint_as_float(q[i + e]) * dd[e] + __uint_as_float(u[i + e]) * om) * (oo[e] * sig));
+        for (int e = 0; e < 2; ++e) {
+          const int at = i + 2 * e;
+          const float2 y = fma2(mul2(pair(q[at], q[at + 1]), both(sig)), dd[e], mul2(mul2(pair(u[at], u[at + 1]), both(sig * om)), oo[e]));
+          u[at / 2] = pack_bf16(y.x, y.y);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; i += 2, out += step) {
-        const uint32_t w = swap(pack_bf16(__uint_as_float(u[i]), __uint_as_float(u[i + 1])));
+        const uint32_t w = swap(u[i / 2]);
         if (i0 + i < n) *reinterpret_cast<uint32_t*>(out) = w;
       }
     }
@@ -523,15 +531,19 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     const uint64_t operand = matrix_at(sm + place * Geo::kBytes, 16), across = matrix_at(sm + place * Geo::kBytes, 8192);
     if (c < chunks) {
     // sigma: the largest element of the column goes to [2^6, 2^7)
-    float top = 0.f;
+    float top = 0.f, other = 0.f;
 #pragma unroll 1
     for (int i = 0; i < kKeys; i += 32) {
       uint32_t r[32];
       tmem_load(my_s + i, r);
       tmem_wait_load();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(r[e])));
+      for (int e = 0; e < 32; e += 4) {
+        top = fmaxf(fmaxf(fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1]))), top);
+        other = fmaxf(fmaxf(fabsf(__uint_as_float(r[e + 2])), fabsf(__uint_as_float(r[e + 3]))), other);
+      }
     }
+    top = fmaxf(top, other);
     most_s[128 * h + row] = top;
     bar_sync(2, 256);
     top = fmaxf(top, most_s[128 * (1 - h) + row]);
@@ -544,7 +556,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
         tmem_load(my_s + i, r);
         tmem_wait_load();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) split2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f, hi[e], lo[e]);
+        for (int e = 0; e < 16; ++e) split2(mul2(pair(r[2 * e], r[2 * e + 1]), both(f)), hi[e], lo[e]);
         tmem_store16(mine + kColSh + (h * kKeys + i) / 2, hi);
         tmem_store16(mine + kColSl + (h * kKeys + i) / 2, lo);
       }
@@ -590,13 +602,13 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       const float4 f = *reinterpret_cast<const float4*>(E + kForget * kC + i), w = *reinterpret_cast<const float4*>(E + kBeta * kC + i);
-      const float ff[4] = {f.x, f.y, f.z, f.w}, ww[4] = {w.x, w.y, w.z, w.w};
-      const uint32_t vv[2] = {swap(v[i / 2]), swap(v[i / 2 + 1])};
+      const float2 ff[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)}, ww[2] = {make_float2(w.x, w.y), make_float2(w.z, w.w)};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y = (e & 1 ? bf16_hi(vv[e / 2]) : bf16_lo(vv[e / 2])) * inv * ww[e] - __uint_as_float(x[i + e]) * ff[e];
-        x[i + e] = __float_as_uint(y);
-        most = fmaxf(most, fabsf(y));
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t two = swap(v[i / 2 + e]);
+        const float2 y = fma2(pair(x[i + 2 * e], x[i + 2 * e + 1]), ff[e], mul2(mul2(make_float2(bf16_lo(two), bf16_hi(two)), both(inv)), ww[e]));
+        x[i + 2 * e] = __float_as_uint(y.x), x[i + 2 * e + 1] = __float_as_uint(y.y);
+        most = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), most);
       }
     }
     most_w[128 * h + row] = most;
@@ -607,7 +619,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     {
       uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) split2(__uint_as_float(x[2 * i]) * back, __uint_as_float(x[2 * i + 1]) * back, hi[i], lo[i]);
+      for (int i = 0; i < 16; ++i) split2(mul2(pair(x[2 * i], x[2 * i + 1]), both(back)), hi[i], lo[i]);
       tmem_store16(mine + kColW + 16 * h, hi);
       tmem_store16(mine + kColW + 32 + 16 * h, lo);
     }
@@ -641,7 +653,10 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
         tmem_load(my_s + i, r);
         tmem_wait_load();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = mul2(pair(r[e], r[e + 1]), both(f));
+          r[e] = __float_as_uint(y.x), r[e + 1] = __float_as_uint(y.y);
+        }
         tmem_store32(my_s + i, r);
       }
     }
@@ -656,17 +671,16 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const float4 k = *reinterpret_cast<const float4*>(E + kKappa * kC + i);
-        x[i] = __float_as_uint(__uint_as_float(x[i]) * k.x), x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * k.y);
-        x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * k.z), x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * k.w);
-        hi[i / 2] = pack_half(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-        hi[i / 2 + 1] = pack_half(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+        const float2 y = mul2(pair(x[i], x[i + 1]), make_float2(k.x, k.y)), z = mul2(pair(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+        x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y), x[i + 2] = __float_as_uint(z.x), x[i + 3] = __float_as_uint(z.y);
+        hi[i / 2] = pack_half(y.x, y.y), hi[i / 2 + 1] = pack_half(z.x, z.y);
       }
       tmem_store16(mine + kColSl + 16 * h, hi);  // its part of the outputs, in place of the state's lower halves
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const float4 l = *reinterpret_cast<const float4*>(E + kLeft * kC + i);
-        split2(__uint_as_float(x[i]) * (l.x * part), __uint_as_float(x[i + 1]) * (l.y * part), hi[i / 2], lo[i / 2]);
-        split2(__uint_as_float(x[i + 2]) * (l.z * part), __uint_as_float(x[i + 3]) * (l.w * part), hi[i / 2 + 1], lo[i / 2 + 1]);
+        split2(mul2(pair(x[i], x[i + 1]), mul2(make_float2(l.x, l.y), both(part))), hi[i / 2], lo[i / 2]);
+        split2(mul2(pair(x[i + 2], x[i + 3]), mul2(make_float2(l.z, l.w), both(part))), hi[i / 2 + 1], lo[i / 2 + 1]);
       }
       tmem_store16(mine + kColW + 16 * h, hi);
       tmem_store16(mine + kColW + 32 + 16 * h, lo);

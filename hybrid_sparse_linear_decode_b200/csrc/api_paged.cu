@@ -66,12 +66,19 @@ struct Plan {
 
 // Up to kNarrowMost rows a KV head: narrow, 8 or 16 rows a warp, bound by the codes' bytes.  More: bf16 on tcgen05, in
 // whose 128 rows one conversion of the codes serves all; fp16, whose weights go in as two parts, on the warps' own
-// products (narrow up to 64 rows, then wide).  While a sequence's rows fit one tile the CTAs share the line of all
-// tiles; more rows, and few row tiles, cut each row tile's tokens into as many parts as fill the SMs, each of at least
-// kLeastTokens.
+// products (narrow up to 64 rows, then wide).  8 sequences of up to 32K tokens, 4 rows a token, narrow / tcgen05: 20
+// rows 162 / 178 us, 32 rows 169 / 179, 48 rows 294 / 208, 64 rows 303 / 204.
+// While a sequence's rows fit one tile the CTAs share the line of all tiles; more rows, and few row tiles, cut each row
+// tile's tokens into as many parts as the SMs hold at once, each of at least kLeastTokens (128 tokens of one sequence,
+// parts of at least 128 / 256 / 512 / 1024 tokens: of 1024 tokens 26 / 23 / 28 / 34 us, of 2048 41 / 30 / 29 / 40).
 constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
-constexpr int kClusterStages = 32;
+// The narrow form by clusters or by the line: a cluster's CTA takes ceil(stages / CTAs) stages of 32 tokens; on the line it
+// takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  One
+// token each, 4096 tokens, 8 KV heads, clusters / line: 8 sequences 18.9 / 21.0 us, 16 28.7 / 32.1; 32 sequences of 2048
+// 34.7 / 32.9, of 1024 20.4 / 22.0; 8 of 16384 49.2 / 52.2, of 32768 94.1 / 93.4.  Clusters above 8 are not used: 4
+// sequences of 4096 in clusters of 13 20.2 / 15.5, 2 in clusters of 16 11.6 / 11.9, 1 of 16384 17.7 / 16.4.
+constexpr int64_t kLineStages = 8;
 
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink, int type) {
   Plan p{};
@@ -91,11 +98,10 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
     const int64_t stages = std::max<int64_t>(1, (len + stage - 1) / stage);
     p.rows = mma ? tile : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     if (!mma) {
-      // each CTA's part of a unit: a stage for each of its warps at least, all units' CTAs on the SMs at once if they
-      // can; short enough that the rest of the time is latency
-      const int64_t most = std::min<int64_t>({kPagedMaxCluster, std::max<int64_t>(1, kSms * kCtasPerSm / units), (stages + 3) / 4});
-      if ((stages + most - 1) / most <= kClusterStages) {
-        p.cluster = (int)most;
+      // each CTA's part of a unit: a stage for each of its warps at least, all units' CTAs on the SMs at once if they can
+      const int64_t slots = kSms * kCtasPerSm, n = std::min<int64_t>(std::max<int64_t>(1, slots / units), (stages + 3) / 4);
+      if (n <= kPagedMaxCluster && (stages + n - 1) / n <= units * stages / slots + kLineStages) {
+        p.cluster = (int)n;
         return p;
       }
     }
@@ -103,7 +109,7 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
     p.bytes = (size_t)2 * p.n_cta * p.rows * row_bytes;
   } else {
     const int64_t tiles = units * ((rows + tile - 1) / tile), all = kSms * (mma ? kMmaCtasPerSm : kCtasPerSm);
-    int64_t n = tiles >= all ? 1 : (all + tiles - 1) / tiles;
+    int64_t n = std::max<int64_t>(1, all / tiles);
     n = std::max<int64_t>(1, std::min<int64_t>({n, len / kLeastTokens, 64}));
     if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
     p.n_splits = (int)n;

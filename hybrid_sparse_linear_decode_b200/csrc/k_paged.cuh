@@ -245,10 +245,6 @@ cudaError_t launch_clusters(void (*f)(A...), dim3 grid, int cluster, dim3 block,
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   c.attrs = attr;
   c.numAttrs = 2;
-  if (cluster > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

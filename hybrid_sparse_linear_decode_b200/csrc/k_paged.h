@@ -62,7 +62,7 @@ struct PagedAttnParams {
 constexpr int kNarrowRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kCtasPerSm = 3;
-constexpr int kPagedMaxCluster = 16;  // above 8 a non-portable size, which this device takes
+constexpr int kPagedMaxCluster = 8;
 // Rows of a CTA of the form on tcgen05.
 constexpr int kMmaRows = 128;
 constexpr int kMmaCtasPerSm = 2;

@@ -11,8 +11,6 @@ namespace {
 // writes the new codes.  So each input is read once and each code written once.
 
 constexpr int kAppendRows = 4;  // rows a thread holds
-constexpr int kRotateThreads = 256;
-constexpr int64_t kRotateApart = 1 << 17;
 
 // a * c - b * s, correctly rounded for 16-bit a and b but for ties within 2^-45:
 // the products' rounding errors are exact (fma), their difference's too (two-sum).
@@ -169,13 +167,6 @@ __device__ __forceinline__ void rotate_queries(const PagedAppendParams& p, int64
   }
 }
 
-template <bool INTERLEAVED, bool HALF>
-__global__ void __launch_bounds__(kRotateThreads, 4) paged_rotate_kernel(const PagedAppendParams p) {
-  pdl_wait_primary();
-  pdl_allow_dependents();
-  rotate_queries<INTERLEAVED, HALF>(p, (int64_t)blockIdx.x * kRotateThreads + threadIdx.x);
-}
-
 template <bool INTERLEAVED, bool HALF, bool INT8>
 __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendParams p) {
   constexpr bool half = HALF;
@@ -310,15 +301,9 @@ cudaError_t append(const PagedAppendParams& p, cudaStream_t s) {
   const int lanes = p.D / 16;
   const int threads = (p.c.P * lanes / kAppendRows + 31) / 32 * 32;
   const int64_t q_threads = p.q != nullptr ? (int64_t)p.b.n_new * ((p.Hq + 3) / 4) * lanes : 0;
-  // Many queries go in a launch of their own, whose fewer registers let more of them be under way (32K tokens of 32
-  // heads: 83 us, the copy bandwidth); for few, one launch less counts more.
-  const bool apart = q_threads >= kRotateApart;
-  const int64_t blocks = p.kv_blocks + (apart ? 0 : (q_threads + threads - 1) / threads);
-  const cudaError_t e = launch(p.int8 ? paged_append_kernel<INTERLEAVED, HALF, true> : paged_append_kernel<INTERLEAVED, HALF, false>,
-                               dim3((unsigned)blocks), dim3(threads), 0, true, s, p);
-  if (!apart || e != cudaSuccess) return e;
-  return launch(paged_rotate_kernel<INTERLEAVED, HALF>, dim3((unsigned)((q_threads + kRotateThreads - 1) / kRotateThreads)),
-                dim3(kRotateThreads), 0, true, s, p);
+  const int64_t blocks = p.kv_blocks + (q_threads + threads - 1) / threads;
+  return launch(p.int8 ? paged_append_kernel<INTERLEAVED, HALF, true> : paged_append_kernel<INTERLEAVED, HALF, false>,
+                dim3((unsigned)blocks), dim3(threads), 0, true, s, p);
 }
 }  // namespace
 

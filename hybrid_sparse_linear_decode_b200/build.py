@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libhyb_attn.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "api_delta.cu", "api_paged.cu", "k_delta.cu", "k_fused.cu", "k_multi.cu", "k_paged.cu", "k_paged_append.cu", "k_paged_mma.cu", "k_select.cu", "k_state.cu"]
-HEADERS = ["hyb_device.cuh", "hyb_internal.h", "k_common.cuh", "k_delta.h", "k_paged.cuh", "k_paged.h", "k_select.h", "k_tcgen05.cuh"]
+HEADERS = ["errors.h", "hyb_device.cuh", "hyb_internal.h", "k_common.cuh", "k_delta.h", "k_paged.cuh", "k_paged.h", "k_select.h", "k_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -15,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/hyb_attn.h"
+#include "errors.h"
 #include "hyb_internal.h"
 #include "k_select.h"
 

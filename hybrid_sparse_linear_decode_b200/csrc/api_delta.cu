@@ -3,6 +3,7 @@
 
 #include <cmath>
 
+#include "errors.h"
 #include "hyb_internal.h"
 #include "k_delta.h"
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "errors.h"
 #include "hyb_internal.h"
 #include "k_paged.h"
 

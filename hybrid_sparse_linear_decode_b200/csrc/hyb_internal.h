@@ -194,7 +194,4 @@ cudaError_t launch_fold(const FoldParams& p, int D, cudaStream_t s);
 // per device, before the first launch: shared-memory size, cluster and carveout attributes
 cudaError_t prepare_state(int D);
 
-// Keeps a failed CUDA call's error for hyb_attn_last_cuda_error; returns HYB_ECUDA.
-int record_cuda_error(cudaError_t e);
-
 }  // namespace hyb

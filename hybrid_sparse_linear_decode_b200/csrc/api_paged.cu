@@ -74,8 +74,9 @@ struct Plan {
 // parts of at least 128 / 256 / 512 / 1024 tokens: of 1024 tokens 26 / 23 / 28 / 34 us, of 2048 41 / 30 / 29 / 40).
 constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
-// The narrow form by clusters or by the line: a cluster's CTA takes ceil(stages / CTAs) stages of 32 tokens; on the line it
-// takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  One
+// The narrow form by clusters or by the line: a cluster's CTA takes stages / CTAs stages of 32 tokens; on the line it
+// takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  (What a
+// length gives to clusters, every shorter one does too, so a window needs no workspace that no window does not.)  One
 // token each, 4096 tokens, 8 KV heads, clusters / line: 8 sequences 18.9 / 21.0 us, 16 28.7 / 32.1; 32 sequences of 2048
 // 34.7 / 32.9, of 1024 20.4 / 22.0; 8 of 16384 49.2 / 52.2, of 32768 94.1 / 93.4.  Clusters above 8 are not used: 4
 // sequences of 4096 in clusters of 13 20.2 / 15.5, 2 in clusters of 16 11.6 / 11.9, 1 of 16384 17.7 / 16.4.
@@ -101,7 +102,7 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
     if (!mma) {
       // each CTA's part of a unit: a stage for each of its warps at least, all units' CTAs on the SMs at once if they can
       const int64_t slots = kSms * kCtasPerSm, n = std::min<int64_t>(std::max<int64_t>(1, slots / units), (stages + 3) / 4);
-      if (n <= kPagedMaxCluster && (stages + n - 1) / n <= units * stages / slots + kLineStages) {
+      if (n <= kPagedMaxCluster && stages * (slots - std::min(slots, units * n)) <= kLineStages * n * slots) {
         p.cluster = (int)n;
         return p;
       }

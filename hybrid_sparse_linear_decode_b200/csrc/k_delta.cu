@@ -40,6 +40,7 @@ __device__ __forceinline__ Run read_run(const DeltaParams& p, int b, bool tell) 
 // rows in a run, so its keys are a contiguous piece of k), reads and writes it once, and takes the tokens
 // through it.  S^T k and S^T q of the old state come from one pass over the registers:
 // u = beta (v - a S^T k), o = scale (a S^T q + (k . q) u), and the second pass forms a S + k u^T.
+// 64 sequences of 32 heads of 128 x 128, one token: 45 us, 6.0 TB/s; one sequence: 3.7 us, latency.
 
 template <int DK>
 struct Piece {
@@ -130,17 +131,28 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
 // with S the state before the chunk.  Then
 //   O = scale (diag(e^G) Q S + P U),  P_ts = e^(G_t - G_s) q_t . k_s for s <= t,
 //   S := e^(G_C) S + K^T diag(e^(G_C - G)) U.
-// One CTA takes a (sequence, head).  Four warps prepare the next chunk (its rows into shared memory, K K^T and
-// Q K^T, T = (I + A)^-1 by 16 x 16 inverses and block products in 32 bits) while the others take the chunk before
-// through the state.  Those hold the state transposed, 16 of its columns a warp, as matrix accumulators, and work on
-// the transposed equations, in which each product's result is the next one's left operand in the registers it is
-// in: X^T = S^T K^T, W^T = (V^T - X^T diag(e^G)) diag(beta), U^T = W^T T^T, O^T, S^T += U^T K.
+// One CTA takes a (sequence, head).  Two groups of four warps prepare chunks in turn, into three places of shared memory:
+// the rows of K and Q, K K^T and Q K^T (on the warps' own matrix instructions, only blocks on and below the diagonal),
+// T = (I + A)^-1 by 16 x 16 inverses and block products in 32 bits.  Eight warps take the chunks through the state on
+// tcgen05.  They hold it transposed in tensor memory, a lane a column of the state, so that the 128 columns are the 128
+// rows of every product and each product's result, read by the lanes it is in and written back as f16, is the next
+// one's left operand:
+//   X^T = S^T K^T,  W^T = (V^T - X^T diag(e^G)) diag(beta),  U^T = W^T T^T,
+//   O^T = S^T Q^T diag(e^G) + U^T P^T,  S^T := e^(G_C) S^T + U^T diag(e^(G_C - G)) K.
+// (A value dimension of 64 leaves the other 64 rows at zero.)  The outputs of a chunk are read while the next one's X is
+// under way, and S decays while U is.
 //
 // Operands are f16.  Rows of K and Q are divided by powers of two kappa that put their largest element in [1, 2), so
-// they go in exactly (but for elements below 2^-17 of it); S, W and T as two f16 parts, 22 bits, after S and W
-// are divided by powers of two of each column of the state (sigma, omega), so that values of any size keep
-// them.  Only O, whose result has 8 bits, takes single parts of S, U and P.  Sums are in 32 bits.  Errors of the
-// state stay near those of 32-bit arithmetic.
+// they go in exactly (but for elements below 2^-17 of it); S, W, T and the U that the state takes as two f16 parts, 22
+// bits, after S and W are divided by powers of two of each column of the state (sigma, omega), so that values of any
+// size keep them.  Only O, whose result has 8 bits, takes single parts of S, U and P.  Sums are in 32 bits.  Errors of
+// the state stay near those of 32-bit arithmetic.
+//
+// What bounds it: the chain from chunk to chunk and the instructions of both sides.  32 heads of 128 x 128 and 8192
+// tokens: 778 us, 11600 clocks a chunk; the scanning warps alone 7700 (their products 1600), the preparing ones alone
+// 7900, 25000 warp instructions in all.  The same products on the warps' own matrix instructions (scan of 6400 clocks at
+// least) took 17800 a chunk; clusters of 4 CTAs that share the columns and pass prepared chunks on 9900 with the
+// machine full, but no less where there are more than 37 heads, the copies (32 bytes a clock from an SM) being the bound.
 
 constexpr int kC = 64, kChunkThreads = 512;  // eight scanning warps, two groups of four that prepare
 

@@ -9,6 +9,12 @@ namespace {
 // 16 channels a thread), reduces their largest magnitude, settles the page's
 // scale, rewrites the codes that the page already holds if the scale grew, and
 // writes the new codes.  So each input is read once and each code written once.
+// CTAs behind those rotate the queries, a thread 16 channels of four heads with one set of angles.
+//
+// Bound by bytes for a prompt, by the chain page table -> row -> scale for a few tokens.  32768 tokens of 32 and 8 heads of
+// 128: 150 us, 5.0 TB/s (of the copies' 6.6); 2 rows a thread 194 us against 171 for 4 when measured.  8 sequences, one
+// token: 2.9 us.  Queries in a launch of their own take longer at all sizes: 2048 tokens 15.0 us against 11.1, 32768 152
+// against 150.
 
 constexpr int kAppendRows = 4;  // rows a thread holds
 

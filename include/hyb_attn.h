@@ -455,7 +455,8 @@ typedef struct hyb_attn_paged_cache {
  * kv_lens[b] - (cu_new[b + 1] - cu_new[b]) and up.  Tokens [i * page_size,
  * (i + 1) * page_size) lie in page page_table[b * table_stride + i].  Rows
  * behind cu_new[batch] are left as they were.  Sequences may share pages that
- * this step only reads; a page that it appends to belongs to one sequence.
+ * this step only reads; a page that it appends to belongs to one sequence, once
+ * (otherwise its codes and scale are some mixture of what was appended).
  * Values that contradict the limits (or each other) are held to them and set
  * HYB_STATUS_BAD_LENGTH; tokens on pages outside the cache are not written, or
  * not seen, and set HYB_STATUS_BAD_PAGE. */
@@ -509,9 +510,14 @@ size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hy
  *   lse    fp32 [n_new][n_q_heads]: log of the sum of exp(scale q . k_j); or NULL
  * A row that sees nothing gets zeros and lse = -inf.  scale 0 selects
  * 1/sqrt(head_dim).  Values are as if in 32 bits but for the softmax weights,
- * which are rounded to 11 bits.  The workspace (16-byte aligned) holds nothing
- * between calls; calls that may run at the same time need one each.
- * Errors: HYB_EINVAL, HYB_ESCRATCH (workspace too small), HYB_ECUDA. */
+ * which are rounded to 11 bits (bf16 rows) or 22 (fp16 rows).  Scales of visible
+ * tokens are finite and not negative, and codes no NaN, as an append leaves them;
+ * what lies in pages behind a sequence's end or outside its window is not used.
+ * The workspace (16-byte aligned; 0 bytes and NULL where the size is 0) holds
+ * nothing between calls; calls that may run at the same time need one each.  A
+ * wait inside the kernel that runs out (about 1 s) sets HYB_STATUS_TIMEOUT in
+ * the batch's status, and the rows are invalid.  Limits: batch * n_kv_heads <=
+ * 65535.  Errors: HYB_EINVAL, HYB_ESCRATCH (workspace too small), HYB_ECUDA. */
 int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
                           const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
                           int32_t n_q_heads, int32_t window, int32_t n_sink, float scale, void* workspace,
@@ -538,7 +544,8 @@ typedef struct hyb_attn_delta_state {
  * state (in place).  Sequence b owns rows [cu_new[b], cu_new[b + 1]) and state
  * slots[b] (slots NULL: state b).  A slot of -1 skips the sequence: its rows and
  * every state are left as they were; other slots outside the states do so too
- * and set HYB_STATUS_BAD_SLOT.  Two sequences of one call never share a slot.
+ * and set HYB_STATUS_BAD_SLOT.  Two sequences of one call never share a slot
+ * (the state would be one's or the other's, element by element).
  *   q, k   bf16 [n_new] rows of [n_k_heads][key_dim]; v: of [n_v_heads][value_dim];
  *          strides in elements, multiples of 8
  *   g, beta fp32 [n_new][n_v_heads]; g <= 0 is a decay's logarithm, -inf forgets
@@ -547,7 +554,9 @@ typedef struct hyb_attn_delta_state {
  *   out    bf16 rows of [n_v_heads][value_dim]
  * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
  * the tokens one by one with the state in registers; long ones in chunks of 64
- * by matrix products.  One launch, no workspace.  Errors: HYB_EINVAL, HYB_ECUDA. */
+ * by matrix products, where a wait that runs out (about 1 s) sets
+ * HYB_STATUS_TIMEOUT and leaves outputs and states invalid.  One launch, no
+ * workspace.  Errors: HYB_EINVAL, HYB_ECUDA. */
 int hyb_attn_delta_run(const hyb_attn_delta_state* state, const void* q, int64_t q_stride, const void* k,
                        int64_t k_stride, const void* v, int64_t v_stride, const float* g, const float* beta,
                        void* out, int64_t out_stride, const int32_t* cu_new, const int32_t* slots, int32_t batch,

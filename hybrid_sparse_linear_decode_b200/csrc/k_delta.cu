@@ -171,7 +171,8 @@ struct ChunkGeo {
 enum { kFull, kFree = 3, kDoneX = 6, kDoneU, kDoneS };
 // Columns of the tensor memory: S^T; as f16, upper and lower halves; X^T, then U^T; Q S; W or U in two parts; P U
 enum { kColS = 0, kColSh = 128, kColSl = 192, kColX = 256, kColQ = 320, kColW = 384, kColP = 448 };
-// The factors' rows: e^G times that of q; -beta e^G kappa; beta; kappa; e^(G_C - G); scale kappa of q; e^G_C
+// The factors' rows: e^G times that of q; -beta e^G kappa; beta; kappa; e^(G_C - G); scale kappa of q; e^G_C and
+// the largest kappa
 enum { kDecay, kForget, kBeta, kKappa, kLeft, kOut, kWhole };
 
 // Byte offset of 16-byte piece c of row r in tiles of 64 rows of 8 pieces, moved so that 8 rows' pieces of one column lie
@@ -389,6 +390,16 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     }
   }
   bar_sync(barrier, 128);
+  // From here on kappa counts in units of its largest, so that what it multiplies stays near 1 for keys of any size.
+  if (warp == 0) {
+    float2* k = reinterpret_cast<float2*>(E + kKappa * kC) + lane;
+    float most = fmaxf(k->x, k->y);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float inv = 1.f / most;
+    *k = make_float2(k->x * inv, k->y * inv);
+    if (lane == 0) E[kWhole * kC + 1] = most;
+  }
   // Blocks of 32, then 64: the lower left of the inverse is -T22 (A21 T11).
   float* M = reinterpret_cast<float*>(smem + Geo::kTmp);
   {
@@ -656,7 +667,8 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     __syncwarp();
     // The state's new unit is the larger of its decayed part's and of U's; meanwhile it decays.
     const float whole = E[kWhole * kC - 32 * h];
-    const float now = fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om);
+    om *= E[kWhole * kC - 32 * h + 1];  // U goes on times kappa
+    const float now = fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om), pow2_of(27));
     {
       const float f = whole * fminf(unit / now, FLT_MAX);
 #pragma unroll 1

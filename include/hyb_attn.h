@@ -506,7 +506,8 @@ size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hy
  * only j > t - W or j < n_sink.  o = sum softmax(scale q . k_j) v_j, query head i
  * on KV head i / (n_q_heads / n_kv_heads).
  *   q      bf16 or fp16 [n_new] rows of [n_q_heads][head_dim], q_stride apart (a
- *          multiple of 8);  out: the same type, out_stride apart (a multiple of 4)
+ *          multiple of 8);  out: the same type, out_stride apart (a multiple of
+ *          4), in other memory than q
  *   lse    fp32 [n_new][n_q_heads]: log of the sum of exp(scale q . k_j); or NULL
  * A row that sees nothing gets zeros and lse = -inf.  scale 0 selects
  * 1/sqrt(head_dim).  Values are as if in 32 bits but for the softmax weights,
@@ -550,8 +551,9 @@ typedef struct hyb_attn_delta_state {
  *          strides in elements, multiples of 8
  *   g, beta fp32 [n_new][n_v_heads]; g <= 0 is a decay's logarithm, -inf forgets
  *          all;  beta the learning rate.  k is taken as it is: for the rule to be
- *          stable |k| <= 1 and 0 <= beta <= 1 (or beta |k|^2 < 2).
- *   out    bf16 rows of [n_v_heads][value_dim]
+ *          stable |k| <= 1 and 0 <= beta <= 1 (or beta |k|^2 < 2).  Values are
+ *          finite: one that is not spoils its sequence's head from up to 63 tokens before.
+ *   out    bf16 rows of [n_v_heads][value_dim], in other memory than the inputs
  * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
  * the tokens one by one with the state in registers; long ones in chunks of 64
  * by matrix products, where a wait that runs out (about 1 s) sets

@@ -2,7 +2,7 @@
 
 Tolerances.  State: each token adds rounding errors of 32-bit dot products of dk terms (random in sign, sqrt(dk) 2^-24
 of their size), the rule contracts them, so after n tokens the norm of a head's error is within 8 sqrt(n dk) 2^-24 of
-the size that went in, |S0| + sqrt(n) max |v| (the 8 covers a few roundings a term and sums of the chunks' 22-bit
+the size that went in, |S0| + sqrt(n) |k| max |v| (the 8 covers a few roundings a term and sums of the chunks' 22-bit
 operands).  Outputs: half a bf16 step of the value, and single f16 parts of state, update and P in the chunks: 2^-11 each of
 sums |S| |q| scale, three of them and the state's error.
 """
@@ -22,7 +22,7 @@ def f64(t):
 
 
 class Delta:
-    def __init__(self, new, Hk=2, Hv=4, dk=64, dv=64, slots=None, n_slots=None, seed=0, size=1.0, forget=0.05, tail=0, wide=0):
+    def __init__(self, new, Hk=2, Hv=4, dk=64, dv=64, slots=None, n_slots=None, seed=0, size=1.0, forget=0.05, tail=0, wide=0, keys=1.0):
         import torch
         import hybrid_sparse_linear_decode_b200 as H
         rng = np.random.default_rng(seed)
@@ -37,13 +37,13 @@ class Delta:
             x = x / np.linalg.norm(x, axis=-1, keepdims=True) if unit else x * size
             return torch.from_numpy(x).cuda().bfloat16()[:, wide // 2:wide // 2 + heads]
 
-        self.q, self.k, self.v = rows(Hk, dk, True), rows(Hk, dk, True), rows(Hv, dv, False)
+        self.q, self.k, self.v = rows(Hk, dk, True), rows(Hk, dk, True) * keys, rows(Hv, dv, False)
         self.g = torch.from_numpy(-forget * rng.exponential(size=(n, Hv)) * rng.uniform(0, 4, (1, Hv))).float().cuda()
         self.beta = torch.from_numpy(rng.uniform(0, 1, (n, Hv))).float().cuda()
         self.state = torch.from_numpy(rng.standard_normal((n_slots, Hv, dk, dv)) * size).float().cuda()
         self.slots = slots
         self.h = H.GatedDeltaState.from_tensor(self.state, n_k_heads=Hk)
-        self.dk, self.dv, self.Hv, self.size = dk, dv, Hv, size
+        self.dk, self.dv, self.Hv, self.size, self.keys = dk, dv, Hv, size, keys
 
     def ints(self, x):
         return self.torch.tensor(np.asarray(x, np.int32), device="cuda")
@@ -70,10 +70,11 @@ class Delta:
             if not m:
                 continue
             rel = 8 * math.sqrt(m * self.dk) * 2.0 ** -24
-            inn = np.linalg.norm(S0[s], axis=(1, 2)) + math.sqrt(m) * np.abs(v).max() * math.sqrt(self.dv)
+            top = self.keys * np.abs(v).max()
+            inn = np.linalg.norm(S0[s], axis=(1, 2)) + math.sqrt(m) * top * math.sqrt(self.dv)
             err = np.linalg.norm(S1[s] - want[s], axis=(1, 2))
             assert (err <= rel * inn).all(), (b, float((err / (rel * inn)).max()))
-            room = 3 * 2.0 ** -11 * (mag + sc * np.abs(v).max()) + (rel * inn * sc)[None, :, None]
+            room = 3 * 2.0 ** -11 * (mag + sc * top) + (rel * inn * sc)[None, :, None]
             assert (np.abs(got[r] - ref) <= 2.0 ** -8 * np.abs(ref) + room).all(), \
                 (b, float((np.abs(got[r] - ref) / (2.0 ** -8 * np.abs(ref) + room)).max()))
         others = [s for s in range(S0.shape[0]) if s not in (range(len(self.new)) if self.slots is None else self.slots)]
@@ -115,6 +116,15 @@ def test_delta_slots(new):
 @pytest.mark.parametrize("size", [1e-12, 1e-4, 3e4, 1e15])
 def test_delta_sizes_of_values(new, size):
     Delta(new, 1, 2, 128, 64, seed=3, size=size).check()
+
+
+@pytest.mark.parametrize("new", [[5, 4], [64], [100, 130]])
+@pytest.mark.parametrize("keys", [2.0 ** -8, 2.0 ** -14, 2.0 ** -30])
+def test_delta_short_keys(new, keys):
+    """Keys far from length 1, into an empty state: what they leave there is held as finely."""
+    d = Delta(new, 1, 2, 128, 128, seed=4, keys=keys)
+    d.state.zero_()
+    d.check()
 
 
 @pytest.mark.parametrize("new", [[6], [150]])

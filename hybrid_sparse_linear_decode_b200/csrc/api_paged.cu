@@ -62,6 +62,7 @@ struct Plan {
   int cluster;   // CTAs a unit (narrow), or 0
   int n_cta;     // line
   int n_splits;  // otherwise
+  int64_t n_whole, row_tiles;  // mma: row tiles taken whole; of a unit
   size_t bytes;
 };
 
@@ -74,6 +75,7 @@ struct Plan {
 // parts of at least 128 / 256 / 512 / 1024 tokens: of 1024 tokens 26 / 23 / 28 / 34 us, of 2048 41 / 30 / 29 / 40).
 constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
+constexpr int kLeastTail = 1024;
 // The narrow form by clusters or by the line: a cluster's CTA takes stages / CTAs stages of 32 tokens; on the line it
 // takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  (What a
 // length gives to clusters, every shorter one does too, so a window needs no workspace that no window does not.)  One
@@ -110,12 +112,25 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
     p.n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(kSms * (mma ? kMmaCtasPerSm : kCtasPerSm), (units * stages + warps - 1) / warps));
     p.bytes = (size_t)2 * p.n_cta * p.rows * row_bytes;
   } else {
-    const int64_t tiles = units * ((rows + tile - 1) / tile), all = kSms * (mma ? kMmaCtasPerSm : kCtasPerSm);
-    int64_t n = std::max<int64_t>(1, all / tiles);
-    n = std::max<int64_t>(1, std::min<int64_t>({n, len / kLeastTokens, 64}));
-    if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
-    p.n_splits = (int)n;
-    p.bytes = n > 1 ? (size_t)n * b->n_new * Hq * row_bytes : 0;
+    p.row_tiles = (rows + tile - 1) / tile;
+    const int64_t tiles = units * p.row_tiles, all = kSms * (mma ? kMmaCtasPerSm : kCtasPerSm);
+    int64_t n = std::max<int64_t>(1, std::min<int64_t>({all / tiles, len / kLeastTokens, 64}));
+    if (!mma) {
+      if (b->max_new > 65535 || b->batch > 65535) n = 1;  // the join's grid
+      p.n_splits = (int)n;
+      p.bytes = n > 1 ? (size_t)n * b->n_new * Hq * row_bytes : 0;
+    } else {
+      // tiles behind the last full turn of the SMs: the parts that take the fewest turns of a part's length
+      const int64_t rest = tiles % all;
+      if (2 * rest > all)
+        for (int64_t i = 2; i <= std::min<int64_t>(8, len / kLeastTail); ++i)
+          if (((rest * i + all - 1) / all) * n < ((rest * n + all - 1) / all) * i) n = i;
+      if (2 * rest <= all && tiles > all && rest > 0)
+        n = std::max<int64_t>(1, std::min<int64_t>({all / rest, len / kLeastTail, 8}));
+      p.n_splits = (int)n;
+      p.n_whole = n > 1 ? tiles - rest : tiles;
+      p.bytes = n > 1 ? (size_t)(rest * n) * tile * row_bytes : 0;
+    }
   }
   return p;
 }
@@ -190,6 +205,7 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   if (lse != nullptr && !aligned(lse, 4)) return HYB_EINVAL;
   if ((int64_t)batch->max_new * (n_q_heads / cache->n_kv_heads) > ((int64_t)1 << 30)) return HYB_EINVAL;
   const Plan plan = make_plan(cache, batch, n_q_heads, window, n_sink, type);
+  if (plan.form == Plan::kMma && (plan.row_tiles * batch->batch * cache->n_kv_heads) * plan.n_splits >= ((int64_t)1 << 31)) return HYB_EINVAL;
   if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes)) return HYB_ESCRATCH;
   if (plan.bytes > 0 && !aligned(workspace, 16)) return HYB_EINVAL;
   PagedAttnParams p{};
@@ -210,6 +226,8 @@ int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_page
   p.n_cta = plan.n_cta;
   p.quantum = plan.form == Plan::kMma ? 1 : 4;
   p.n_splits = plan.n_splits;
+  p.n_whole = (int)plan.n_whole;
+  p.row_tiles = (int)plan.row_tiles;
   p.ws = static_cast<float*>(workspace);
   p.status = batch->status;
   const int int8 = cache->code == HYB_CODE_INT8;

@@ -726,6 +726,45 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   if (threadIdx.x < D / 4) store_joined(p, tok, hd, D, threadIdx.x, y, m, l);
 }
 
+// Joins the parts of the row tiles from n_whole on (at most 64 parts).  One warp a row.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_tiles_kernel(const PagedAttnParams p) {
+  const int units = p.b.B * p.c.Hkv, tile = p.n_whole + blockIdx.x, unit = tile % units;
+  const int b = unit / p.c.Hkv, h = unit % p.c.Hkv, lane = threadIdx.x & 31, n = p.n_splits;
+  const int in_tile = 4 * blockIdx.y + (threadIdx.x >> 5), row = (p.row_tiles - 1 - tile / units) * kMmaRows + in_tile;
+  bool bad;
+  const Seq seq = read_seq(p.b, b, p.c.P, &bad);
+  pdl_wait_primary();
+  if (row >= seq.n * p.G) return;
+  const float* parts = p.ws + ((int64_t)blockIdx.x * n * kMmaRows + in_tile) * (D + 4);
+  constexpr int64_t kNext = (int64_t)kMmaRows * (D + 4);
+  float2 e[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    e[k] = lane + 32 * k < n ? *reinterpret_cast<const float2*>(parts + (lane + 32 * k) * kNext + D) : make_float2(-INFINITY, 0.f);
+  float m = fmaxf(e[0].x, e[1].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float w[2], l;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) w[k] = m == -INFINITY ? 0.f : exp2_fast(e[k].x - m) * e[k].y;
+  l = w[0] + w[1];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
+    if (lane < D / 4) {
+      const float4 o = *reinterpret_cast<const float4*>(parts + i * kNext + 4 * lane);
+      y.x += f * o.x, y.y += f * o.y, y.z += f * o.z, y.w += f * o.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+  if (lane < D / 4) store_joined(p, seq.t0 + row / p.G, h * p.G + row % p.G, D, lane, y, m, l);
+}
+
 // ---- the wide form: many rows a KV head --------------------------------------------------------------
 //
 // A CTA takes 64 rows, 16 a warp, and passes the stages its rows can see through
@@ -874,7 +913,7 @@ cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
                          dim3(kWarps * 32), smem, true, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  return launch_paged_join_rows(p, D, s);
+  return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(kJoinThreads), 0, true, s, p);
 }
 
 }  // namespace
@@ -885,9 +924,9 @@ cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStr
   if (D == 128) return launch(paged_join_kernel<128, 128>, grid, block, 0, true, s, p, rows);
   return launch(paged_join_kernel<64, 128>, grid, block, 0, true, s, p, rows);
 }
-cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s) {
-  const dim3 grid(p.Hq, p.b.max_new, p.b.B), block(kJoinThreads);
-  return D == 128 ? launch(paged_join_rows_kernel<128>, grid, block, 0, true, s, p) : launch(paged_join_rows_kernel<64>, grid, block, 0, true, s, p);
+cudaError_t launch_paged_join_tiles(const PagedAttnParams& p, int D, cudaStream_t s) {
+  const dim3 grid(p.b.B * p.c.Hkv * p.row_tiles - p.n_whole, kMmaRows / 4), block(kJoinThreads);
+  return D == 128 ? launch(paged_join_tiles_kernel<128>, grid, block, 0, true, s, p) : launch(paged_join_tiles_kernel<64>, grid, block, 0, true, s, p);
 }
 
 cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int rows, cudaStream_t s) {

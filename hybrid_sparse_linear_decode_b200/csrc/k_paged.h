@@ -52,7 +52,8 @@ struct PagedAttnParams {
   int32_t cluster;   // CTAs of a cluster that takes one unit (narrow form), or 0
   int32_t n_cta;     // CTAs that share the line of all units' stages
   int32_t quantum;   // stages that a CTA's part is a multiple of
-  int32_t n_splits;  // parts of each row tile's stages (wide forms)
+  int32_t n_splits;  // parts of a row tile's stages: of each (wide form), of those from n_whole on (tcgen05)
+  int32_t n_whole, row_tiles;  // tcgen05: row tiles taken whole; of each sequence and KV head
   float* ws;         // partial results
   uint32_t* status;
 };
@@ -72,8 +73,9 @@ cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int r
 cudaError_t launch_paged_mma(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s);
 
-// Joins of the parts that several CTAs left: of the line of 128-token tiles with `rows` rows a unit; of n_splits parts.
+// Joins of the parts that several CTAs left: of the line of 128-token tiles with `rows` rows a unit; of n_splits
+// parts of every row; of row tiles from n_whole on.
 cudaError_t launch_paged_join(const PagedAttnParams& p, int D, int rows, cudaStream_t s);
-cudaError_t launch_paged_join_rows(const PagedAttnParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged_join_tiles(const PagedAttnParams& p, int D, cudaStream_t s);
 
 }  // namespace hyb

@@ -48,13 +48,14 @@ __device__ __forceinline__ bool warp_wait(const PagedAttnParams& p, uint64_t* ba
 }
 
 // ---- the pieces of work of a CTA ---------------------------------------------------------------------------
-// With splits: one piece, part `split` of one row tile's tiles of tokens.  Without (n_cta > 0): this CTA's part of the
-// line of all units' tiles, where every sequence has at most 128 rows a KV head; as many pieces as units in it.
+// n_cta > 0: this CTA's part of the line of all units' tiles, where every sequence has at most 128 rows a KV head; as
+// many pieces as units in it.  Otherwise one piece: a row tile, or a part of one of the last.  Row tiles go by what they
+// see, all units' last ones first.
 struct Piece {
   Seq seq;
   Span<kTile> span;
   int b, h, row0, rows, s0, s1;
-  int64_t slot;   // line: where a part's result goes
+  int64_t slot;   // where a part's result goes
   bool complete;  // the piece is all of its row tile's tiles
 };
 struct Work {
@@ -92,19 +93,22 @@ __device__ __forceinline__ bool next_piece(const PagedAttnParams& p, Work& w, Pi
   } else {
     if (w.done) return false;
     w.done = true;
-    const int unit = blockIdx.y, tiles = (int)(gridDim.x / p.n_splits), split = (int)(blockIdx.x % p.n_splits);
+    const int units = p.b.B * p.c.Hkv, late = (int)blockIdx.x - p.n_whole;  // from 0: parts
+    const int tile = late < 0 ? (int)blockIdx.x : p.n_whole + late / p.n_splits;
+    const int splits = late < 0 ? 1 : p.n_splits, split = late < 0 ? 0 : late % p.n_splits;
+    const int unit = tile % units;
     x.b = unit / p.c.Hkv, x.h = unit % p.c.Hkv;
     x.seq = read_seq(p.b, x.b, p.c.P, &bad);
     x.rows = x.seq.n * p.G;
-    x.row0 = (tiles - 1 - (int)(blockIdx.x / p.n_splits)) * kTile;  // the tiles that see most come first
+    x.row0 = (p.row_tiles - 1 - tile / units) * kTile;
     if (x.row0 >= x.rows) return false;
     const int pos0 = x.seq.len - x.seq.n;
     const int lo = pos0 + x.row0 / p.G, hi = pos0 + (min(x.rows, x.row0 + kTile) - 1) / p.G;
     x.span = hi >= 0 ? make_span<kTile>(max(lo, 0), hi, p.W, p.S) : Span<kTile>{0, 0, 0, 0, 0};
-    x.s0 = (int)((int64_t)x.span.stages * split / p.n_splits);
-    x.s1 = (int)((int64_t)x.span.stages * (split + 1) / p.n_splits);
-    x.complete = p.n_splits == 1;
-    x.slot = split;
+    x.s0 = (int)((int64_t)x.span.stages * split / splits);
+    x.s1 = (int)((int64_t)x.span.stages * (split + 1) / splits);
+    x.complete = splits == 1;
+    x.slot = late;
   }
   if (bad && x.h == 0 && x.s0 == 0 && x.row0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
   return true;
@@ -431,7 +435,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
     }
     // the row's result
     const float f = l == 0.f ? 0.f : pow2_of(ref) / l;
-    float* ws = p.n_cta > 0 ? p.ws + (x.slot * kTile + row) * (D + 4) : p.ws + ((x.slot * p.b.n_new + tok) * p.Hq + hd) * (D + 4);
+    float* ws = p.ws + (x.slot * kTile + row - x.row0) * (D + 4);
     if (any) {
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -506,11 +510,8 @@ __global__ void __launch_bounds__(kThreads, kMmaCtasPerSm) paged_mma_kernel(cons
 
 template <int D, bool INT8>
 cudaError_t run(const PagedAttnParams& p, cudaStream_t s) {
-  dim3 grid(p.n_cta);
-  if (p.n_cta == 0) {
-    const int64_t tiles = ((int64_t)p.b.max_new * p.G + kTile - 1) / kTile;
-    grid = dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv);
-  }
+  const unsigned late = (unsigned)p.b.B * p.c.Hkv * p.row_tiles - p.n_whole;
+  const dim3 grid(p.n_cta > 0 ? p.n_cta : p.n_whole + late * p.n_splits);
   return launch(paged_mma_kernel<D, INT8>, grid, dim3(kThreads), MmaGeo<D>::kTotal, true, s, p);
 }
 
@@ -523,7 +524,7 @@ cudaError_t launch_paged_mma(const PagedAttnParams& p, int D, int int8, cudaStre
   else
     e = int8 ? run<64, true>(p, s) : run<64, false>(p, s);
   if (e != cudaSuccess || (p.n_cta == 0 && p.n_splits == 1)) return e;
-  return p.n_cta > 0 ? launch_paged_join(p, D, kTile, s) : launch_paged_join_rows(p, D, s);
+  return p.n_cta > 0 ? launch_paged_join(p, D, kTile, s) : launch_paged_join_tiles(p, D, s);
 }
 
 }  // namespace hyb

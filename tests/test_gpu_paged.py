@@ -356,6 +356,18 @@ def test_attend_many_sequences():
     c.check_attend([1 if n else 0 for n in lens], 4)
 
 
+@pytest.mark.parametrize("lens,new,Hkv,G,window", [
+    ([2300], [330], 8, 8, 0),               # 168 row tiles: fewer than the SMs hold, in parts
+    ([2100, 90], [640, 90], 4, 8, 0),       # 320, many of them without rows; the last ones in parts
+    ([2200], [620], 8, 8, 0),               # 312, whole but for the last 16
+    ([2500], [330], 8, 8, 700),             # as the first, behind a window
+    ([9000], [17], 1, 8, 0)])               # 2, in many parts
+def test_attend_row_tiles_in_parts(lens, new, Hkv, G, window):
+    c = Paged(lens, 64, Hkv, 64, "e4m3", "bf16", seed=13)
+    c.check_attend(new, Hkv * G, window, 5, tail=1)
+    assert c.h.status() == 0
+
+
 def test_attend_long_cache_and_far_pages():
     """A cache whose codes lie past 2^31 bytes, and a sequence whose tokens do."""
     import torch

@@ -160,7 +160,7 @@ def test_no_new_rows_is_no_work(A):
     assert A.hyb_attn_paged_workspace_size(c, b, 4) == 0
 
 
-@pytest.mark.parametrize("B,new,G", [(1, 1, 1), (3, 4, 4), (8, 1, 4), (100, 1, 4), (2, 40, 8), (64, 1, 8), (1, 700, 1)])
+@pytest.mark.parametrize("B,new,G", [(1, 1, 1), (3, 4, 4), (8, 1, 4), (100, 1, 4), (2, 40, 8), (64, 1, 8), (1, 700, 1), (2, 1500, 8), (8, 600, 4)])
 def test_workspace_of_a_window_fits_the_workspace_asked_for(A, B, new, G):
     """The workspace size does not depend on the window, which only shrinks the work: a call with one takes the same
     buffer (it reaches the launch, which fails here without a GPU, instead of the workspace check)."""

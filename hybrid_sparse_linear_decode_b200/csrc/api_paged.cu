@@ -75,6 +75,9 @@ struct Plan {
 // parts of at least 128 / 256 / 512 / 1024 tokens: of 1024 tokens 26 / 23 / 28 / 34 us, of 2048 41 / 30 / 29 / 40).
 constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
+// On tcgen05, row tiles that fill the SMs more than half, or come behind full turns of them, go in parts of at least
+// kLeastTail tokens (512 / 1024 / 2048 / whole: 2047 tokens of 10001 608 / 608 / 608 / 639 us, 1300 of 8192 335 / 334 / 325 /
+// 440, 1300 of 4096 171 / 172 / 189 / 211, 700 of 4096 141 / 129 / 144 / 144, 2048 of 2048 136 / 98 / 98 / 98).
 constexpr int kLeastTail = 1024;
 // The narrow form by clusters or by the line: a cluster's CTA takes stages / CTAs stages of 32 tokens; on the line it
 // takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  (What a

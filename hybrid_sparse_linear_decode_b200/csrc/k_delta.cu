@@ -209,22 +209,27 @@ __device__ __forceinline__ uint32_t field_of(float x, uint32_t lo, uint32_t hi) 
 __device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
 
 // Rows of K or Q, four 16-byte pieces of each thread at a time: loaded, and divided by their kappa and stored as f16.
-// The pieces of a row lie in DK / 8 lanes.
+// The pieces of a row lie in DK / 8 lanes; a thread's are kStep rows apart, a multiple of 8, so all in one column.
+template <int DK>
+struct RowPieces {
+  static constexpr int kStep = 128 / (DK / 8);
+};
 template <int DK>
 __device__ __forceinline__ void load_rows(uint4 (&w)[4], const uint16_t* src, int64_t stride, int n, int first, int tid) {
-  constexpr int kPieces = DK / 8;
+  constexpr int kPieces = DK / 8, kStep = RowPieces<DK>::kStep;
+  int r = tid / kPieces + first * kStep;
+  src += r * stride + tid % kPieces * 8;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = tid + 128 * (first + i), r = at / kPieces, c = at % kPieces;
-    w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + r * stride + c * 8)) : make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i, r += kStep, src += kStep * stride)
+    w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
 }
 template <int DK>
 __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, float* kappa, int first, int tid) {
-  constexpr int kPieces = DK / 8;
+  constexpr int kPieces = DK / 8, kStep = RowPieces<DK>::kStep;
+  tile += tile_at(tid / kPieces, tid % kPieces) + first * (kStep * 128);
+  kappa += tid / kPieces + first * kStep;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int at = tid + 128 * (first + i), r = at / kPieces, c = at % kPieces;
     const uint32_t z[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     uint32_t top = 0;  // magnitudes of bf16 order as integers
 #pragma unroll
@@ -239,8 +244,8 @@ __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, f
       const float2 w = mul2(make_float2(bf16_lo(z[x]), bf16_hi(z[x])), inv);
       y[x] = pack_half(w.x, w.y);
     }
-    *reinterpret_cast<uint4*>(tile + tile_at(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (c == 0) kappa[r] = pow2_of(e);
+    *reinterpret_cast<uint4*>(tile + i * kStep * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (tid % kPieces == 0) kappa[i * kStep] = pow2_of(e);
   }
 }
 

@@ -209,14 +209,12 @@ __device__ __forceinline__ uint32_t field_of(float x, uint32_t lo, uint32_t hi) 
 __device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
 
 // Rows of K or Q, four 16-byte pieces of each thread at a time: loaded, and divided by their kappa and stored as f16.
-// The pieces of a row lie in DK / 8 lanes; a thread's are kStep rows apart, a multiple of 8, so all in one column.
+// The pieces of a row lie in DK / 8 lanes; a thread's are kRowStep rows apart, a multiple of 8, so all in one column.
 template <int DK>
-struct RowPieces {
-  static constexpr int kStep = 128 / (DK / 8);
-};
+constexpr int kRowStep = 128 / (DK / 8);
 template <int DK>
 __device__ __forceinline__ void load_rows(uint4 (&w)[4], const uint16_t* src, int64_t stride, int n, int first, int tid) {
-  constexpr int kPieces = DK / 8, kStep = RowPieces<DK>::kStep;
+  constexpr int kPieces = DK / 8, kStep = kRowStep<DK>;
   int r = tid / kPieces + first * kStep;
   src += r * stride + tid % kPieces * 8;
 #pragma unroll
@@ -225,7 +223,7 @@ __device__ __forceinline__ void load_rows(uint4 (&w)[4], const uint16_t* src, in
 }
 template <int DK>
 __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, float* kappa, int first, int tid) {
-  constexpr int kPieces = DK / 8, kStep = RowPieces<DK>::kStep;
+  constexpr int kPieces = DK / 8, kStep = kRowStep<DK>;
   tile += tile_at(tid / kPieces, tid % kPieces) + first * (kStep * 128);
   kappa += tid / kPieces + first * kStep;
 #pragma unroll
@@ -458,10 +456,10 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       *reinterpret_cast<float4*>(A + (32 + y + r) * kLd + x) = make_float4(-s[r][0].x, -s[r][0].y, -s[r][1].x, -s[r][1].y);
     bar_sync(barrier, 128);
   }
-  // T in two parts; zeros above the diagonal
+  // T in two parts, in blocks of 16 x 16 on and below the diagonal: two threads a row, so a warp's rows are of one block
+  const int y = tid >> 1;
 #pragma unroll 1
-  for (int i = tid; i < kC * 8; i += 128) {
-    const int y = i >> 3, c = i & 7;
+  for (int c = tid & 1; c < 2 * warp + 2; c += 2) {
     const float4 u = *reinterpret_cast<const float4*>(A + y * kLd + 8 * c), w = *reinterpret_cast<const float4*>(A + y * kLd + 8 * c + 4);
     const float a[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
     uint32_t hi[4], lo[4];

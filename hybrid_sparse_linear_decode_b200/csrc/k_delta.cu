@@ -247,10 +247,27 @@ __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, f
   }
 }
 
-// Prepares the chunk of n tokens from `row` on in `buf`; this group's next one has `next` tokens from row `ahead` on.
+// What a group has under way of its next chunk: the first rows of K; the first warp two tokens' g and beta a lane.
+struct Ahead {
+  uint4 rows[4];
+  float g0, g1, b0, b1;
+};
 template <int DK>
-__device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* smem, uint8_t* buf, int barrier, int row, int n, int ahead,
-                                              int next, int hk, int hv, int tid) {
+__device__ __forceinline__ void begin_chunk(const DeltaParams& p, Ahead& a, int row, int n, int hk, int hv, int tid) {
+  load_rows<DK>(a.rows, p.k + (int64_t)row * p.k_stride + (int64_t)hk * DK, p.k_stride, n, 0, tid);
+  if (tid < 32) {
+    const int r0 = 2 * tid, r1 = r0 + 1;
+    const int64_t at = (int64_t)(row + r0) * p.Hv + hv;
+    a.g0 = r0 < n ? __ldg(p.g + at) : 0.f, a.g1 = r1 < n ? __ldg(p.g + at + p.Hv) : 0.f;
+    a.b0 = r0 < n ? __ldg(p.beta + at) : 0.f, a.b1 = r1 < n ? __ldg(p.beta + at + p.Hv) : 0.f;
+  }
+}
+
+// Prepares the chunk of n tokens from `row` on, which begin_chunk has begun, in `buf`; this group's next one has `next`
+// tokens from row `ahead` on, and is begun here.
+template <int DK>
+__device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* smem, uint8_t* buf, Ahead& under_way, int barrier, int row,
+                                              int n, int ahead, int next, int hk, int hv, int tid) {
   using Geo = ChunkGeo<DK>;
   constexpr int kLd = Geo::kLd;
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -263,8 +280,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
   constexpr int kSteps = DK / 64;  // of each
   const uint16_t* from_k = p.k + (int64_t)row * p.k_stride + (int64_t)hk * DK;
   const uint16_t* from_q = p.q + (int64_t)row * p.q_stride + (int64_t)hk * DK;
-  uint4 rows[4];
-  load_rows<DK>(rows, from_k, p.k_stride, n, 0, tid);
+  uint4(&rows)[4] = under_way.rows;
   // the next chunk on its way into L2, a line of 128 bytes at a time
   for (int i = tid; i < next * (DK / 64); i += 128) {
     const int64_t r = ahead + i / (DK / 64);
@@ -279,11 +295,8 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
   // the sums of g in powers of two and in 64 bits, kept as two floats so that their differences keep 32; a
   // decay of e^-200 is 0 in 32 bits like any stronger one.  Two tokens a lane.
   const int r0 = 2 * lane, r1 = r0 + 1;
-  float b0 = 0.f, b1 = 0.f;
+  const float b0 = under_way.b0, b1 = under_way.b1, g0 = under_way.g0, g1 = under_way.g1;
   if (warp == 0) {
-    const int64_t at = (int64_t)(row + r0) * p.Hv + hv;
-    const float g0 = r0 < n ? p.g[at] : 0.f, g1 = r1 < n ? p.g[at + p.Hv] : 0.f;
-    b0 = r0 < n ? p.beta[at] : 0.f, b1 = r1 < n ? p.beta[at + p.Hv] : 0.f;
     const double kLog2e64 = 1.4426950408889634;
     const double a = (g0 < -200.f ? -200. : (double)g0) * kLog2e64, c = (g1 < -200.f ? -200. : (double)g1) * kLog2e64;
     double sum = a + c;
@@ -456,6 +469,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       *reinterpret_cast<float4*>(A + (32 + y + r) * kLd + x) = make_float4(-s[r][0].x, -s[r][0].y, -s[r][1].x, -s[r][1].y);
     bar_sync(barrier, 128);
   }
+  if (next > 0) begin_chunk<DK>(p, under_way, ahead, next, hk, hv, tid);
   // T in two parts, in blocks of 16 x 16 on and below the diagonal: two threads a row, so a warp's rows are of one block
   const int y = tid >> 1;
 #pragma unroll 1
@@ -775,6 +789,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunks_kernel(const De
   } else {
     const int group = (warp - 8) >> 2, me = tid & 127;
     int* go = reinterpret_cast<int*>(smem + Geo::kTmem + 4 + 4 * group);
+    Ahead under_way{};
+    if (group < chunks) begin_chunk<DK>(p, under_way, run.t0 + group * kC, min(run.n - group * kC, kC), hk, hv, me);
 #pragma unroll 1
     for (int c = group; c < chunks; c += 2) {
       const int place = c % 3, next = c + 2;
@@ -787,7 +803,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunks_kernel(const De
         bar_sync(3 + group, 128);
         if (*go == 0) break;
       }
-      chunk_prepare<DK>(p, smem + Geo::kWork + group * Geo::kWorkBytes, smem + place * Geo::kBytes, 3 + group, run.t0 + c * kC,
+      chunk_prepare<DK>(p, smem + Geo::kWork + group * Geo::kWorkBytes, smem + place * Geo::kBytes, under_way, 3 + group, run.t0 + c * kC,
                         min(run.n - c * kC, kC), run.t0 + next * kC, min(max(run.n - next * kC, 0), kC), hk, hv, me);
       fence_smem();
       __syncwarp();

@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
 // the state stay near those of 32-bit arithmetic.
 //
 // What bounds it: the chain from chunk to chunk and the instructions of both sides.  32 heads of 128 x 128 and 8192
-// tokens: 778 us, 11600 clocks a chunk; the scanning warps alone 7700 (their products 1600), the preparing ones alone
-// 7900, 25000 warp instructions in all.  The same products on the warps' own matrix instructions (scan of 6400 clocks at
+// tokens: 738 us, 11000 clocks a chunk; the scanning warps alone 7500 (their products 1600), the preparing ones alone
+// 8300, 23300 warp instructions in all.  The same products on the warps' own matrix instructions (scan of 6400 clocks at
 // least) took 17800 a chunk; clusters of 4 CTAs that share the columns and pass prepared chunks on 9900 with the
 // machine full, but no less where there are more than 37 heads, the copies (32 bytes a clock from an SM) being the bound.
 
@@ -247,16 +247,24 @@ __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, f
   }
 }
 
-// What a group has under way of its next chunk: the first rows of K; the first warp two tokens' g and beta a lane.
+// What a group has under way of its next chunk: the rows' first two steps (four pieces of each thread a step: K's, then
+// Q's); the last warp two tokens' g and beta a lane.
 struct Ahead {
-  uint4 rows[4];
+  uint4 even[4], odd[4];
   float g0, g1, b0, b1;
 };
 template <int DK>
+__device__ __forceinline__ void load_step(const DeltaParams& p, uint4 (&w)[4], int step, int row, int n, int hk, int tid) {
+  const bool of_q = step >= DK / 64;
+  const int64_t stride = of_q ? p.q_stride : p.k_stride;
+  load_rows<DK>(w, (of_q ? p.q : p.k) + row * stride + (int64_t)hk * DK, stride, n, 4 * (step % (DK / 64)), tid);
+}
+template <int DK>
 __device__ __forceinline__ void begin_chunk(const DeltaParams& p, Ahead& a, int row, int n, int hk, int hv, int tid) {
-  load_rows<DK>(a.rows, p.k + (int64_t)row * p.k_stride + (int64_t)hk * DK, p.k_stride, n, 0, tid);
-  if (tid < 32) {
-    const int r0 = 2 * tid, r1 = r0 + 1;
+  load_step<DK>(p, a.even, 0, row, n, hk, tid);
+  load_step<DK>(p, a.odd, 1, row, n, hk, tid);
+  if (tid >= 96) {
+    const int r0 = 2 * (tid - 96), r1 = r0 + 1;
     const int64_t at = (int64_t)(row + r0) * p.Hv + hv;
     a.g0 = r0 < n ? __ldg(p.g + at) : 0.f, a.g1 = r1 < n ? __ldg(p.g + at + p.Hv) : 0.f;
     a.b0 = r0 < n ? __ldg(p.beta + at) : 0.f, a.b1 = r1 < n ? __ldg(p.beta + at + p.Hv) : 0.f;
@@ -276,11 +284,6 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
   float* Ghi = reinterpret_cast<float*>(smem + Geo::kG);
   float* Glo = Ghi + kC;
   float* kq = Glo + kC;
-  // the chunk's rows, past its end zeros: K's four pieces at a time, then Q's
-  constexpr int kSteps = DK / 64;  // of each
-  const uint16_t* from_k = p.k + (int64_t)row * p.k_stride + (int64_t)hk * DK;
-  const uint16_t* from_q = p.q + (int64_t)row * p.q_stride + (int64_t)hk * DK;
-  uint4(&rows)[4] = under_way.rows;
   // the next chunk on its way into L2, a line of 128 bytes at a time
   for (int i = tid; i < next * (DK / 64); i += 128) {
     const int64_t r = ahead + i / (DK / 64);
@@ -292,11 +295,25 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     const int lines = p.DV / 64;
     prefetch_l2(p.v + (int64_t)(ahead + i / lines) * p.v_stride + (int64_t)hv * p.DV + i % lines * 64);
   }
-  // the sums of g in powers of two and in 64 bits, kept as two floats so that their differences keep 32; a
-  // decay of e^-200 is 0 in 32 bits like any stronger one.  Two tokens a lane.
-  const int r0 = 2 * lane, r1 = r0 + 1;
-  const float b0 = under_way.b0, b1 = under_way.b1, g0 = under_way.g0, g1 = under_way.g1;
-  if (warp == 0) {
+  // the chunk's rows, past its end zeros
+#pragma unroll 1
+  for (int i = 0; i < DK / 64; ++i) {
+    auto store = [&](const uint4 (&w)[4], int step) {
+      const bool of_q = step >= DK / 64;
+      store_rows<DK>(w, buf + (of_q ? Geo::kQ : Geo::kK), of_q ? kq : E + kKappa * kC, 4 * (step % (DK / 64)), tid);
+    };
+    store(under_way.even, 2 * i);
+    if (i + 1 < DK / 64) load_step<DK>(p, under_way.even, 2 * i + 2, row, n, hk, tid);
+    store(under_way.odd, 2 * i + 1);
+    if (i + 1 < DK / 64) load_step<DK>(p, under_way.odd, 2 * i + 3, row, n, hk, tid);
+  }
+  bar_sync(barrier, 128);
+  // The sums of g in powers of two and in 64 bits, kept as two floats so that their differences keep 32; a
+  // decay of e^-200 is 0 in 32 bits like any stronger one.  Two tokens a lane of the last warp, while the others begin
+  // the products.
+  if (warp == 3) {
+    const int r0 = 2 * lane, r1 = r0 + 1;
+    const float b0 = under_way.b0, b1 = under_way.b1, g0 = under_way.g0, g1 = under_way.g1;
     const double kLog2e64 = 1.4426950408889634;
     const double a = (g0 < -200.f ? -200. : (double)g0) * kLog2e64, c = (g1 < -200.f ? -200. : (double)g1) * kLog2e64;
     double sum = a + c;
@@ -308,31 +325,13 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     const double end = __shfl_sync(0xffffffffu, sum, 31), s0 = sum - c;
     Ghi[r0] = (float)s0, Ghi[r1] = (float)sum;
     Glo[r0] = (float)(s0 - (double)(float)s0), Glo[r1] = (float)(sum - (double)(float)sum);
-    E[kDecay * kC + r0] = exp2f((float)s0), E[kDecay * kC + r1] = exp2f((float)sum);
+    const float d0 = exp2f((float)s0), d1 = exp2f((float)sum), o0 = p.scale * kq[r0], o1 = p.scale * kq[r1];
+    E[kForget * kC + r0] = -b0 * d0 * E[kKappa * kC + r0], E[kForget * kC + r1] = -b1 * d1 * E[kKappa * kC + r1];
+    E[kOut * kC + r0] = o0, E[kOut * kC + r1] = o1;
+    E[kDecay * kC + r0] = d0 * o0, E[kDecay * kC + r1] = d1 * o1;
     E[kLeft * kC + r0] = exp2f((float)(end - s0)), E[kLeft * kC + r1] = exp2f((float)(end - sum));
     E[kBeta * kC + r0] = b0, E[kBeta * kC + r1] = b1;
     if (lane == 0) E[kWhole * kC] = exp2f((float)end);
-  }
-#pragma unroll 1
-  for (int i = 0; i < 2 * kSteps; ++i) {
-    const bool of_q = i >= kSteps, then_q = i + 1 >= kSteps;
-    uint4 then[4];
-    if (i + 1 < 2 * kSteps)
-      load_rows<DK>(then, then_q ? from_q : from_k, then_q ? p.q_stride : p.k_stride, n, 4 * ((i + 1) % kSteps), tid);
-    store_rows<DK>(rows, buf + (of_q ? Geo::kQ : Geo::kK), of_q ? kq : E + kKappa * kC, 4 * (i % kSteps), tid);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) rows[x] = then[x];
-  }
-  bar_sync(barrier, 128);
-  if (warp == 0) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = r0 + x;
-      const float decay = E[kDecay * kC + r], out = p.scale * kq[r];
-      E[kForget * kC + r] = -(x ? b1 : b0) * decay * E[kKappa * kC + r];
-      E[kOut * kC + r] = out;
-      E[kDecay * kC + r] = decay * out;
-    }
   }
 
   // K K^T and Q K^T below the diagonal, in blocks of 16 x 16: first this warp's own on the diagonal, then the six others in turn
@@ -345,7 +344,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t a[4], c[4], b[4];
       const int at = tile_at(16 * bi + (lane & 15), 2 * ks + (lane >> 4));
@@ -357,6 +356,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
       mma_f16(qk[0], c, b[0], b[1]);
       mma_f16(qk[1], c, b[2], b[3]);
     }
+    if (i < 4) bar_sync(barrier, 128);  // the sums of g are there
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int y = 16 * bi + g + 8 * r;
@@ -406,16 +406,6 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     }
   }
   bar_sync(barrier, 128);
-  // From here on kappa counts in units of its largest, so that what it multiplies stays near 1 for keys of any size.
-  if (warp == 0) {
-    float2* k = reinterpret_cast<float2*>(E + kKappa * kC) + lane;
-    float most = fmaxf(k->x, k->y);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float inv = 1.f / most;
-    *k = make_float2(k->x * inv, k->y * inv);
-    if (lane == 0) E[kWhole * kC + 1] = most;
-  }
   // Blocks of 32, then 64: the lower left of the inverse is -T22 (A21 T11).
   float* M = reinterpret_cast<float*>(smem + Geo::kTmp);
   {
@@ -445,7 +435,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     const int y = (tid >> 3) * 2, x = (tid & 7) * 4;  // two rows and 4 columns
     auto product = [&](const float* left, const float* right, int ld, float2 (&s)[2][2]) {
       s[0][0] = s[0][1] = s[1][0] = s[1][1] = both(0.f);
-#pragma unroll 1
+#pragma unroll 2
       for (int l = 0; l < 32; l += 4) {
         const float4 u = *reinterpret_cast<const float4*>(left + l), w = *reinterpret_cast<const float4*>(left + kLd + l);
         const float a[4] = {u.x, u.y, u.z, u.w}, c[4] = {w.x, w.y, w.z, w.w};
@@ -470,6 +460,17 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     bar_sync(barrier, 128);
   }
   if (next > 0) begin_chunk<DK>(p, under_way, ahead, next, hk, hv, tid);
+  // What is done with kappa from here on takes it in units of its largest, so that what it multiplies stays near 1 for keys of
+  // any size.  (The first warp has the least of what follows.)
+  if (warp == 0) {
+    float2* k = reinterpret_cast<float2*>(E + kKappa * kC) + lane;
+    float most = fmaxf(k->x, k->y);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float inv = 1.f / most;
+    *k = make_float2(k->x * inv, k->y * inv);
+    if (lane == 0) E[kWhole * kC + 1] = most;
+  }
   // T in two parts, in blocks of 16 x 16 on and below the diagonal: two threads a row, so a warp's rows are of one block
   const int y = tid >> 1;
 #pragma unroll 1

@@ -31,7 +31,8 @@ __device__ __forceinline__ float diff_of_products(float a, float c, float b, flo
 
 template <bool INT8>
 __device__ __forceinline__ float scale_for(float amax) {
-  if (INT8) return fmaxf(__fdiv_rn(amax, 127.f), 1.17549435e-38f);
+  // times 1 / 127, as a tensor divided by a number is computed: a unit in the last place would turn ties of codes
+  if (INT8) return fmaxf(__fmul_rn(amax, 1.f / 127.f), 1.17549435e-38f);
   // the smallest power of two x in [2^-126, 2^126] with amax <= 448 x:
   // 448 = 1.75 * 2^8, so x = 2^(e - 8) or the next for amax = m 2^e, 1 <= m < 2
   const uint32_t u = __float_as_uint(amax);

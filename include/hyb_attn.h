@@ -426,7 +426,7 @@ const char* hyb_attn_strerror(int code);
  * A value is code * scale, with one scale per page and KV head, for keys and
  * values apart.  e4m3 codes: the scale is the smallest power of two (2^-126 ..
  * 2^126) with |x| <= 448 * scale for all x of the page; int8 codes: the largest
- * |x| / 127 (2^-126 at least).
+ * |x| times 1 / 127 in 32 bits (2^-126 at least).
  * ======================================================================== */
 #define HYB_CODE_E4M3 0
 #define HYB_CODE_INT8 1

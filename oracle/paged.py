@@ -38,7 +38,7 @@ def encode(y: np.ndarray, kind: str) -> np.ndarray:
 
 def scale_for(amax: float, kind: str) -> float:
     if kind == "int8":
-        return max(float(np.float32(amax) / np.float32(127)), 2.0 ** -126)
+        return max(float(np.float32(amax) * (np.float32(1) / np.float32(127))), 2.0 ** -126)
     x = -126
     while 448.0 * 2.0 ** x < amax:
         x += 1

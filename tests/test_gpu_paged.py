@@ -184,6 +184,24 @@ def test_append_token_by_token_grows_scales(kind):
             break
 
 
+def test_append_int8_ties():
+    """Codes halfway between two, and scales where a division by 127 and a product with 1 / 127 differ."""
+    import torch
+    c = Paged([0] * 3, 16, 2, 64, "int8", "bf16", seed=21)
+    x = (torch.arange(128, 256).double() / 128).float()      # all significands of bf16
+    turn = x[x / torch.full_like(x, 127.0) != x * (torch.ones(1) / torch.full((1,), 127.0))]
+    assert len(turn) >= 3
+    n = 3 * 16
+    v = torch.zeros(n, 2, 64)
+    for page in range(3):
+        for h in range(2):
+            top = turn[(2 * page + h) % len(turn)]
+            v[16 * page:16 * page + 16, h] = torch.cat([top / 2 ** torch.arange(8.0), -top / 2 ** torch.arange(8.0)]).repeat(64).view(16, 64)
+    rows = v.cuda().bfloat16()
+    assert torch.equal(rows.float().cpu(), v)
+    check_append(c, [0, 0, 0], [16, 16, 16], k=rows, v=rows)
+
+
 def test_append_again_is_the_same():
     import torch
     c = Paged([50], 16, 2, 128, "e4m3", "bf16", seed=2)

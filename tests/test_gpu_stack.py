@@ -145,3 +145,53 @@ def test_stack(kind):
                 sel = O.select_blocks(O.block_scores(q[b, rows], mu, var, 1 / math.sqrt(D)), k)
                 ref = O.hybrid_subtract(q[b, rows], K[b, h, :T], V[b, h, :T], part, sel, 1 / math.sqrt(D))
                 assert np.abs(o[b, rows] - ref).max() <= 2e-3
+
+
+def test_two_streams_at_once():
+    """Prompts, single tokens and appends of handles of their own on two streams at once give what they give alone."""
+    import torch
+    import hybrid_sparse_linear_decode_b200 as H
+    gen = torch.Generator("cuda").manual_seed(8)
+    lens, news = [700, 333], [[200, 333], [1, 1]]
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def make(d):
+        table = torch.arange(2 * 11, device="cuda").view(2, 11).int()
+        steps = []
+        for new in news:
+            n = sum(new)
+            k = torch.nn.functional.normalize(rand(n, 2, d), dim=-1).bfloat16()
+            steps.append((ints([0, new[0], n]), max(new), rand(n, 16, d).bfloat16(), k, rand(n, 2, d).bfloat16(), -0.1 * rand(n, 2).abs(),
+                          torch.rand(n, 2, generator=gen, device="cuda")))
+        first = torch.randint(-127, 128, (22, 2, 64, d), generator=gen, device="cuda", dtype=torch.int8)
+        return table, ints(lens), first, steps
+
+    def run(made, stream=None):
+        table, held, first, steps = made
+        scale = torch.full(first.shape[:2], 0.01, device="cuda")
+        cache = H.PagedKVCache.from_tensors(first.clone(), first.clone(), scale, scale.clone())
+        states = H.GatedDeltaState(2, 2, 2, first.shape[3], first.shape[3])
+        torch.cuda.synchronize()
+        outs = []
+        for cu, most, q, k, v, g, beta in steps:
+            for _ in range(4):
+                cache.append(k, v, cu, held, table, max_new=most, stream=stream)
+                outs.append(cache.attend(q, cu, held, table, max_new=most, max_len=max(lens), stream=stream))
+                outs.append(states.run(q[:, :2], k, v, g, beta, cu, max_new=most, stream=stream))
+        return outs + [cache.k_pages, cache.v_pages, states.state], (cache, states)
+
+    made = [make(64), make(128)]
+    alone = [run(m)[0] for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(3):
+        both = [run(m, s) for m, s in zip(made, streams)]
+        torch.cuda.synchronize()
+        for (got, handles), want in zip(both, alone):
+            assert all(h.status() == 0 for h in handles)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))

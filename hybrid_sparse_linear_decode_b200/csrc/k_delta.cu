@@ -344,7 +344,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
-#pragma unroll 4
+#pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t a[4], c[4], b[4];
       const int at = tile_at(16 * bi + (lane & 15), 2 * ks + (lane >> 4));
@@ -591,7 +591,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     s = pow2_of(field_of(top * unit, 127 - 30, 127 + 110) - 6);
     {
       const float f = fminf(unit / s, FLT_MAX);
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < kKeys; i += 32) {
         uint32_t r[32], hi[16], lo[16];
         tmem_load(my_s + i, r);
@@ -689,7 +689,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     const float now = fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om), pow2_of(27));
     {
       const float f = whole * fminf(unit / now, FLT_MAX);
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < kKeys; i += 32) {
         uint32_t r[32];
         tmem_load(my_s + i, r);

@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
 // the state stay near those of 32-bit arithmetic.
 //
 // What bounds it: the chain from chunk to chunk and the instructions of both sides.  32 heads of 128 x 128 and 8192
-// tokens: 738 us, 11000 clocks a chunk; the scanning warps alone 7500 (their products 1600), the preparing ones alone
-// 8300, 23300 warp instructions in all.  The same products on the warps' own matrix instructions (scan of 6400 clocks at
+// tokens: 700 us, 10400 clocks a chunk; the scanning warps alone 7300 (their products 1600), the preparing ones alone
+// 7600, 22100 warp instructions in all.  The same products on the warps' own matrix instructions (scan of 6400 clocks at
 // least) took 17800 a chunk; clusters of 4 CTAs that share the columns and pass prepared chunks on 9900 with the
 // machine full, but no less where there are more than 37 heads, the copies (32 bytes a clock from an SM) being the bound.
 
@@ -207,6 +207,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // Exponent field of x, held to [lo, hi] (NaN and infinity: hi), and its power of two.
 __device__ __forceinline__ uint32_t field_of(float x, uint32_t lo, uint32_t hi) { return min(max(__float_as_uint(x) >> 23, lo), hi); }
 __device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
+// 1 / x of a power of two x from 2^-126 to 2^126.
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // Rows of K or Q, four 16-byte pieces of each thread at a time: loaded, and divided by their kappa and stored as f16.
 // The pieces of a row lie in DK / 8 lanes; a thread's are kRowStep rows apart, a multiple of 8, so all in one column.
@@ -467,7 +469,7 @@ __device__ __forceinline__ void chunk_prepare(const DeltaParams& p, uint8_t* sme
     float most = fmaxf(k->x, k->y);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float inv = 1.f / most;
+    const float inv = pow2_inverse(most);
     *k = make_float2(k->x * inv, k->y * inv);
     if (lane == 0) E[kWhole * kC + 1] = most;
   }
@@ -590,7 +592,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     top = fmaxf(top, most_s[128 * (1 - h) + row]);
     s = pow2_of(field_of(top * unit, 127 - 30, 127 + 110) - 6);
     {
-      const float f = fminf(unit / s, FLT_MAX);
+      const float f = fminf(unit * pow2_inverse(s), FLT_MAX);
 #pragma unroll
       for (int i = 0; i < kKeys; i += 32) {
         uint32_t r[32], hi[16], lo[16];
@@ -638,7 +640,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     uint32_t x[32];
     tmem_load(mine + kColX + 32 * h, x);
     tmem_wait_load();
-    const float inv = 1.f / sig;
+    const float inv = pow2_inverse(sig);
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -656,7 +658,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     bar_sync(2, 256);
     most = fmaxf(most, most_w[128 * (1 - h) + row]);
     om = pow2_of(field_of(most, 127 - 60, 127 + 96) - 6);
-    const float back = 1.f / om;
+    const float back = pow2_inverse(om);
     {
       uint32_t hi[16], lo[16];
 #pragma unroll
@@ -686,9 +688,10 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     // The state's new unit is the larger of its decayed part's and of U's; meanwhile it decays.
     const float whole = E[kWhole * kC - 32 * h];
     om *= E[kWhole * kC - 32 * h + 1];  // U goes on times kappa
-    const float now = fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om), pow2_of(27));
+    const float now = fminf(fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om), pow2_of(27)), pow2_of(253));
+    const float by = pow2_inverse(now);
     {
-      const float f = whole * fminf(unit / now, FLT_MAX);
+      const float f = whole * fminf(unit * by, FLT_MAX);
 #pragma unroll
       for (int i = 0; i < kKeys; i += 32) {
         uint32_t r[32];
@@ -708,7 +711,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     tmem_load(mine + kColX + 32 * h, x);
     tmem_wait_load();
     {
-      const float part = sig * om / now;
+      const float part = sig * om * by;
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {

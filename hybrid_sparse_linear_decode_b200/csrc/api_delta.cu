@@ -12,7 +12,8 @@ using namespace hyb;
 namespace {
 
 // From this many tokens a sequence the chunks are faster than single steps: 4 sequences of 32 heads of 128 x 128, steps /
-// chunks: 8 tokens 9.5 / 13.7 us, 16 15.6 / 13.8, 64 51.8 / 14.2; 32 sequences 62.6 / 94.9, 106.8 / 95.7, 375 / 104.
+// chunks: 8 tokens 9.4 / 13.1 us, 12 12.5 / 13.1, 16 15.4 / 13.1, 64 51.7 / 13.5; 32 sequences: 8 tokens 62.5 / 91.2, 12 84.8 /
+// 91.6, 16 106.7 / 91.7, 64 375 / 97.
 constexpr int kChunksFrom = 14;
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

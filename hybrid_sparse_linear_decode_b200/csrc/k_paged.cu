@@ -134,7 +134,7 @@ template <int D, int NT>
 struct Rows {
   float o[NT][D / 16][4];  // channels (D / 8) g + 2 j (elements 0, 1) and the next (2, 3), g = lane / 4
   float m[NT][2], l[NT][2], rf[NT][2];
-  int pos[NT][2];        // position, or -1 for a row that is not there
+  int pos[NT][2];        // position, or -1 for a row that is not there or lies before its sequence
   uint32_t ref;          // exponent field of the value scales' reference
   int pos_min, pos_max;  // of the warp's rows that are there
 
@@ -214,7 +214,7 @@ __device__ __forceinline__ void make_rows(const PagedAttnParams& p, const RawRow
     for (int c = 0; c < 2; ++c) {
       R.rf[n][c] = pow2_of(__shfl_sync(0xffffffffu, e, (2 * t + c) * 4)) * p.scale;
       const int r = row_first + 8 * n + 2 * t + c;
-      R.pos[n][c] = r < rows ? pos0 + r / p.G : -1;
+      R.pos[n][c] = r < rows ? max(pos0 + r / p.G, -1) : -1;
     }
   }
   R.pos_min = row_first < rows ? pos0 + row_first / p.G : 0;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
   Line line{};
   uint32_t first = 0, last = 1, at = 0;
   if (p.cluster == 0) {
-    line = make_line<kStageTokens>(p);
+    line = make_line<kStageTokens>(p, blockIdx.x == 0 && threadIdx.x < 32);
     first = at = min(line.per * blockIdx.x, line.total);
     last = min(first + line.per, line.total);
   }
@@ -494,10 +494,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
       s0 = min(part * rank, span.stages), s1 = min(s0 + part, span.stages);
       complete = p.cluster == 1;
       at = last;
+      if (bad && h == 0 && rank == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
     }
-    const int rows = min(seq.n * p.G, kRows), pos0 = seq.len - seq.n;
+    const int rows = min(seq.n * p.G, kRows), pos0 = seq.pos0;
     const int32_t* table = p.b.table + (int64_t)b * p.b.mp;
-    if (bad && h == 0 && s0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
 
     // the queries, then the first stages
     RawRows<D, NT> raw;
@@ -705,11 +705,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
     return;
   }
   // the line up to this sequence
-  const Line line = make_line<T>(p);
+  const Line line = make_line<T>(p, false);
   uint32_t begin = __shfl_sync(0xffffffffu, line.before, b & 31);
   if (b >= 32) {
     uint32_t sum = 0;
-    for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_stages<T>(p, i);
+    for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_stages<T>(p, i, false);
     begin = warp_sum(sum);
   }
   begin += (uint32_t)h * stages;
@@ -791,10 +791,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
   bool bad;
   const Seq seq = read_seq(p.b, b, p.c.P, &bad);
   if (bad && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
-  const int rows = seq.n * p.G, row0 = tile * kWideRows, pos0 = seq.len - seq.n;
+  const int rows = seq.n * p.G, row0 = tile * kWideRows, pos0 = seq.pos0;
   if (row0 >= rows) return;
   const int pos_min = pos0 + row0 / p.G, pos_max = pos0 + (min(rows, row0 + kWideRows) - 1) / p.G;
-  const Span<kStageTokens> span = pos_max >= 0 ? make_span<kStageTokens>(max(pos_min, 0), pos_max, p.W, p.S) : Span<kStageTokens>{0, 0, 0, 0, 0};
+  const Span<kStageTokens> span = pos_max >= 0 ? make_span<kStageTokens>(max(pos_min, 0), pos_max, seq.cap, p.W, p.S) : Span<kStageTokens>{0, 0, 0, 0, 0};
   const int s0 = (int)((int64_t)span.stages * split / p.n_splits);
   const int s1 = (int)((int64_t)span.stages * (split + 1) / p.n_splits);
   const int32_t* table = p.b.table + (int64_t)b * p.b.mp;

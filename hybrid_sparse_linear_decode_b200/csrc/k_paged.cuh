@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <climits>
 
 #include "hyb_device.cuh"
 #include "k_paged.h"
@@ -32,20 +33,25 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool half) {
 
 // ---- a sequence of the step --------------------------------------------------------------------
 struct Seq {
-  int t0, n, len;  // first row, new tokens, tokens in all
+  int t0, n;  // first row, new tokens
+  int pos0;   // position of the first row
+  int cap;    // tokens that the page table has room for
 };
 
-// Reads a sequence's ranges and holds them within what the caller said: rows
-// within [0, n_new), at most max_new of them, a length within the page table.
+// Reads a sequence's ranges and holds its rows within what the caller said: within [0, n_new), at most max_new of
+// them.  A row keeps its position, lens - cu[i + 1] + row, whatever else is held: what falls outside [0, cap) is for the
+// caller to skip.  Positions from pos0 to pos0 + n fit 32 bits (those below -2^30 are as good as -2^30, n being at most
+// 2^30).
 __device__ __forceinline__ Seq read_seq(const PagedBatch& b, int i, int P, bool* bad) {
   Seq s;
   const int c0 = b.cu[i], c1 = b.cu[i + 1], len = b.lens[i];
   s.t0 = min(max(c0, 0), b.n_new);
   const int t1 = min(max(c1, s.t0), b.n_new);
   s.n = min(t1 - s.t0, b.max_new);
-  const int64_t cap = (int64_t)b.mp * P;
-  s.len = (int)min((int64_t)max(len, 0), cap);
-  *bad = s.t0 != c0 || s.n != c1 - c0 || s.len != len;
+  s.cap = b.mp * P;  // at most 2^30
+  s.pos0 = (int)min(max((int64_t)len - c1 + s.t0, -((int64_t)1 << 30)), (int64_t)INT_MAX - s.n);
+  const int64_t n = (int64_t)c1 - c0;
+  *bad = s.t0 != c0 || s.n != n || len > s.cap || len < n;
   return s;
 }
 
@@ -90,11 +96,11 @@ struct Span {
   int sink, lo, hi, sink_stages, stages;
 };
 template <int T>
-__device__ __forceinline__ Span<T> make_span(int pos_min, int pos_max, int W, int S) {
+__device__ __forceinline__ Span<T> make_span(int pos_min, int pos_max, int cap, int W, int S) {
   Span<T> s;
-  s.hi = pos_max + 1;
+  s.hi = min(pos_max + 1, cap);
   s.lo = W > 0 ? max(pos_min - W + 1, 0) & ~15 : 0;
-  s.sink = W > 0 ? min(S, s.lo) : 0;
+  s.sink = W > 0 ? min(S, min(s.lo, s.hi)) : 0;  // positions past the table may have lo > hi
   s.sink_stages = (s.sink + T - 1) / T;
   s.stages = s.sink_stages + (max(s.hi - s.lo, 0) + T - 1) / T;
   return s;
@@ -116,8 +122,8 @@ __device__ __forceinline__ void stage_range(const Span<T>& s, int st, int& base,
 
 template <int T>
 __device__ __forceinline__ Span<T> seq_span(const PagedAttnParams& p, const Seq& s) {
-  if (s.n == 0) return Span<T>{0, 0, 0, 0, 0};
-  return make_span<T>(max(s.len - s.n, 0), s.len - 1, p.W, p.S);
+  if (s.n == 0 || s.pos0 + s.n <= 0) return Span<T>{0, 0, 0, 0, 0};
+  return make_span<T>(max(s.pos0, 0), s.pos0 + s.n - 1, s.cap, p.W, p.S);
 }
 
 // The line's geometry, in all lanes of a warp.  Stage counts fit 31 bits (the host
@@ -129,11 +135,12 @@ struct Line {
   uint32_t before;
 };
 
-// Stages of all of a sequence's units.
+// Stages of all of a sequence's units.  `tell`: what contradicts the caller's limits goes to the status.
 template <int T>
-__device__ __forceinline__ uint32_t seq_stages(const PagedAttnParams& p, int b) {
+__device__ __forceinline__ uint32_t seq_stages(const PagedAttnParams& p, int b, bool tell) {
   bool bad;
   const Seq s = read_seq(p.b, b, p.c.P, &bad);
+  if (bad && tell) raise(p.status, HYB_STATUS_BAD_LENGTH);
   return (uint32_t)seq_span<T>(p, s).stages * (uint32_t)p.c.Hkv;
 }
 __device__ __forceinline__ uint32_t warp_sum(uint32_t x) {
@@ -151,17 +158,17 @@ __device__ __forceinline__ uint32_t warp_upto(uint32_t x) {  // inclusive prefix
   return x;
 }
 template <int T>
-__device__ __forceinline__ Line make_line(const PagedAttnParams& p) {
+__device__ __forceinline__ Line make_line(const PagedAttnParams& p, bool tell) {
   const int lane = threadIdx.x & 31;
   Line l;
-  l.mine = lane < p.b.B ? seq_stages<T>(p, lane) : 0;
+  l.mine = lane < p.b.B ? seq_stages<T>(p, lane, tell) : 0;
   const uint32_t upto = warp_upto(l.mine);
   l.before = upto - l.mine;
   l.total = __shfl_sync(0xffffffffu, upto, 31);
   if (p.b.B > 32) {
     uint32_t sum = 0;
 #pragma unroll 1
-    for (int b = 32 + lane; b < p.b.B; b += 32) sum += seq_stages<T>(p, b);
+    for (int b = 32 + lane; b < p.b.B; b += 32) sum += seq_stages<T>(p, b, tell);
     l.total += warp_sum(sum);
   }
   const uint32_t n = (uint32_t)(p.n_cta * p.quantum);
@@ -181,7 +188,7 @@ __device__ __forceinline__ int line_find(const PagedAttnParams& p, const Line& l
   uint32_t before = __shfl_sync(0xffffffffu, l.before + l.mine, 31);
 #pragma unroll 1
   for (int b0 = 32; b0 < p.b.B; b0 += 32) {
-    const uint32_t mine = b0 + lane < p.b.B ? seq_stages<T>(p, b0 + lane) : 0;
+    const uint32_t mine = b0 + lane < p.b.B ? seq_stages<T>(p, b0 + lane, false) : 0;
     const uint32_t upto = before + warp_upto(mine);
     past = __ballot_sync(0xffffffffu, upto > x);
     if (past) {

@@ -155,7 +155,7 @@ __device__ __forceinline__ void rotate_queries(const PagedAppendParams& p, int64
   if (t < s.t0 || t >= s.t0 + s.n) return;  // a row behind the last sequence
   Angles a;
   if (r.angle >= 0) {
-    const int pos = s.len - s.n + (int)(t - s.t0);
+    const int pos = s.pos0 + (int)(t - s.t0);
     if (pos < 0 || pos >= p.n_pos) raise(p.status, HYB_STATUS_BAD_LENGTH);
     load_angles(a, p.rope + (int64_t)min(max(pos, 0), p.n_pos - 1) * p.rot, p.rot, r.angle);
   }
@@ -198,11 +198,10 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendPara
   bool bad;
   const Seq s = read_seq(p.b, b, P, &bad);
   if (bad && pi == 0 && h == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
-  const int start = s.len - s.n;  // position of the first new token
-  const int first = max(start, 0);
-  if (start < 0 && pi == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
-  const int pg = first / P + pi;  // page of the sequence
-  const int lo = max(pg * P, first), hi = (int)min((int64_t)(pg + 1) * P, (int64_t)s.len);
+  const int start = s.pos0, first = max(start, 0);  // positions of the first new token, and of the first that has one
+  const int pg = first / P + pi;                    // page of the sequence
+  if (pg >= p.b.mp) return;                         // tokens past the table are skipped
+  const int lo = max(pg * P, first), hi = min((pg + 1) * P, start + s.n);
   if (lo >= hi) return;
   const int j = threadIdx.x % lanes, row0 = threadIdx.x / lanes, step = blockDim.x / lanes;
   const Runs r = lane_runs(j, values ? 0 : p.rot, INTERLEAVED);

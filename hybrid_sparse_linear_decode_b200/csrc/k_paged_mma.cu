@@ -66,7 +66,7 @@ struct Work {
 __device__ __forceinline__ void start_work(const PagedAttnParams& p, Work& w) {
   w.done = false;
   if (p.n_cta > 0) {
-    w.line = make_line<kTile>(p);
+    w.line = make_line<kTile>(p, blockIdx.x == 0 && threadIdx.x < 32);
     w.first = min(w.line.per * blockIdx.x, w.line.total);
     w.last = min(w.first + w.line.per, w.line.total);
     w.at = w.first;
@@ -101,16 +101,16 @@ __device__ __forceinline__ bool next_piece(const PagedAttnParams& p, Work& w, Pi
     x.seq = read_seq(p.b, x.b, p.c.P, &bad);
     x.rows = x.seq.n * p.G;
     x.row0 = (p.row_tiles - 1 - tile / units) * kTile;
+    if (bad && x.h == 0 && x.row0 == 0 && split == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
     if (x.row0 >= x.rows) return false;
-    const int pos0 = x.seq.len - x.seq.n;
+    const int pos0 = x.seq.pos0;
     const int lo = pos0 + x.row0 / p.G, hi = pos0 + (min(x.rows, x.row0 + kTile) - 1) / p.G;
-    x.span = hi >= 0 ? make_span<kTile>(max(lo, 0), hi, p.W, p.S) : Span<kTile>{0, 0, 0, 0, 0};
+    x.span = hi >= 0 ? make_span<kTile>(max(lo, 0), hi, x.seq.cap, p.W, p.S) : Span<kTile>{0, 0, 0, 0, 0};
     x.s0 = (int)((int64_t)x.span.stages * split / splits);
     x.s1 = (int)((int64_t)x.span.stages * (split + 1) / splits);
     x.complete = splits == 1;
     x.slot = late;
   }
-  if (bad && x.h == 0 && x.s0 == 0 && x.row0 == 0 && threadIdx.x == 0) raise(p.status, HYB_STATUS_BAD_LENGTH);
   return true;
 }
 
@@ -276,11 +276,11 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
   bool alive = true, ok = true;  // after a wait that ran out the warps keep the barriers' count, and wait for nothing more
 #pragma unroll 1
   while (next_piece(p, w, x)) {
-    const int row = x.row0 + tid, pos0 = x.seq.len - x.seq.n;
+    const int row = x.row0 + tid, pos0 = x.seq.pos0;
     const bool there = row < x.rows, any = x.row0 + 32 * warp < x.rows;
     const int64_t tok = x.seq.t0 + (there ? row / p.G : 0);
     const int hd = x.h * p.G + (there ? row % p.G : 0);
-    const int pos = there ? pos0 + row / p.G : -1;
+    const int pos = there ? max(pos0 + row / p.G, -1) : -1;
     float m = -INFINITY, l = 0.f;
     uint32_t ref = 1;
     if (x.s0 < x.s1) {
@@ -336,7 +336,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
           auto seen = [&](int c) {
             const int at = base + 32 * c;
             uint32_t see = low_bits(pos - at + 1) & (low_bits(live[2 * c]) | (low_bits(live[2 * c + 1]) << 16));
-            if (p.W > 0) see &= ~low_bits(pos - p.W + 1 - at) | low_bits(p.S - at);
+            if (p.W > 0) see &= ~low_bits(max(pos - at + 1, 0) - p.W) | low_bits(p.S - at);
             return see;
           };
           // The tile's maximum.  Loops are not unrolled: a warp alone on its scheduler runs straight code at the rate

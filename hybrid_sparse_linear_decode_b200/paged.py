@@ -21,8 +21,9 @@ class PagedKVCache:
 
     A step's sequences are given by three int32 device tensors: ``cu`` [B + 1] (sequence b owns token rows
     cu[b] .. cu[b + 1]), ``kv_lens`` [B] (its tokens once the new ones are counted) and ``page_table`` [B, pages].
-    ``max_new`` and ``max_len`` bound a sequence's new tokens and tokens in all.  What contradicts the bounds or the
-    table is held to them or skipped, and noted in ``status``.
+    ``max_new`` and ``max_len`` bound a sequence's new tokens and tokens in all.  Rows past ``max_new`` and tokens at
+    positions or on pages that the table or the cache does not have are skipped, and noted in ``status``; the others keep
+    their positions.
     """
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,

@@ -76,7 +76,7 @@ extern "C" {
 /* bits of the caller's own status word (paged cache and delta rule calls) */
 #define HYB_STATUS_BAD_PAGE      0x20u /* a page index outside the cache (its tokens are skipped) */
 #define HYB_STATUS_BAD_SLOT      0x80u /* a state index outside the states, other than -1 (sequence skipped) */
-#define HYB_STATUS_BAD_LENGTH    0x40u /* lengths or row ranges outside what the call was told (held to it) */
+#define HYB_STATUS_BAD_LENGTH    0x40u /* lengths or row ranges outside what the call was told (the rest is skipped) */
 
 /* ---- failure injection for tests (hyb_attn_set_test_flags) ---------------- */
 #define HYB_TEST_WITHHOLD_SCORES 0x1u  /* rank 1 of every unit's cluster does not hand its block
@@ -457,9 +457,12 @@ typedef struct hyb_attn_paged_cache {
  * behind cu_new[batch] are left as they were.  Sequences may share pages that
  * this step only reads; a page that it appends to belongs to one sequence, once
  * (otherwise its codes and scale are some mixture of what was appended).
- * Values that contradict the limits (or each other) are held to them and set
- * HYB_STATUS_BAD_LENGTH; tokens on pages outside the cache are not written, or
- * not seen, and set HYB_STATUS_BAD_PAGE. */
+ * Values that contradict the limits (or each other) set HYB_STATUS_BAD_LENGTH, in
+ * whatever sequence they are.  No row takes another position for it: rows outside
+ * [0, n_new) and those past a sequence's first max_new are skipped, and so are
+ * tokens at positions outside [0, table_stride * page_size), which an append does
+ * not write and an attention does not see.  Tokens on pages outside the cache are
+ * not written, or not seen, and set HYB_STATUS_BAD_PAGE. */
 typedef struct hyb_attn_paged_batch {
   const int32_t* page_table;  /* [batch][table_stride] */
   const int32_t* cu_new;      /* [batch + 1], rising, from 0 to at most n_new */

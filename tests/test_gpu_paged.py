@@ -272,6 +272,64 @@ def test_append_leaves_rows_behind_the_last_sequence():
     assert (out[4:] == 5).all() and not (out[:4] == 5).all() and c.h.status() == 0
 
 
+# Sequences that contradict what the call was told: cu, kv_lens, max_new, and the position of each row that counts.  Tables of
+# four pages of 16 have room for 64 tokens.
+CONTRADICTIONS = [
+    ([0, 1], [65], 1, 1, {}),                          # one token past the table
+    ([0, 4], [66], 4, 4, {0: 62, 1: 63}),              # a run that passes the table's end
+    ([0, 3], [1 << 30], 3, 3, {}),
+    ([0, 3], [(1 << 31) - 1], 3, 3, {}),
+    ([0, 5], [30], 5, 2, {0: 25, 1: 26}),              # more rows than max_new
+    ([0, 20], [41], 20, 17, {i: 21 + i for i in range(17)}),
+    ([0, 4], [2], 4, 4, {2: 0, 3: 1}),                 # more new tokens than tokens
+    ([0, 4], [0], 4, 4, {}),
+    ([0, 4], [-5], 4, 4, {}),
+    ([-2, 3], [10], 5, 5, {0: 7, 1: 8, 2: 9}),         # rows before the first
+    ([0, 9], [20], 4, 4, {i: 11 + i for i in range(4)}),   # and behind the last
+    ([3, 1], [20], 4, 4, {}),                          # a range that falls
+    ([-(1 << 31), (1 << 31) - 1], [20], 4, 4, {}),
+]
+
+
+@pytest.mark.parametrize("cu,lens,rows,max_new,pos", CONTRADICTIONS)
+def test_append_contradictions_move_no_token(cu, lens, rows, max_new, pos):
+    """Rows without a place are skipped; the others keep their positions, and older tokens their codes."""
+    import hybrid_sparse_linear_decode_b200 as H
+    c = Paged([64], 16, 2, 64, seed=23)
+    k, v, q = c.rows(rows, 2), c.rows(rows, 2), c.rows(rows, 4)
+    rope = angles(80, 64)
+    out = c.torch.full_like(q, 3.0)
+    c.h.append(k, v, c.ints(cu), c.ints(lens), c.ints(c.table[:, :4]), max_new=max_new, rope=rope, q=q, q_out=out)
+    assert c.h.status() == H.HYB_STATUS_BAD_LENGTH
+    if pos:
+        first, n = min(pos), len(pos)
+        at = np.arange(pos[first], pos[first] + n)
+        table = f64(rope).astype(np.float32)
+        kk = OP.rotate(f64(k[first:first + n]), table, at, False).astype(np.float32)
+        OP.append(c.codes["k"], c.scales["k"], kk, int(at[0]), c.table[0], c.kind, c.page)
+        OP.append(c.codes["v"], c.scales["v"], f64(v[first:first + n]).astype(np.float32), int(at[0]), c.table[0], c.kind, c.page)
+        ref = OP.rotate(f64(q[first:first + n]), table, at, False)
+        tol = HALF[c.dtype] * np.abs(ref) + 2.0 ** -22 * np.abs(f64(q[first:first + n])).max(-1, keepdims=True)
+        assert (np.abs(f64(out[first:first + n]) - ref) <= tol).all()
+    for x in "kv":
+        assert np.array_equal(c.t[x].view(c.torch.uint8).cpu().numpy(), c.codes[x]), x
+        assert np.array_equal(c.ts[x].cpu().numpy(), c.scales[x], equal_nan=True), x
+
+
+def test_append_contradictions_of_one_sequence_leave_the_others():
+    import hybrid_sparse_linear_decode_b200 as H
+    c = Paged([64, 64, 64], 16, 1, 64, seed=24)
+    k = c.rows(6, 1)
+    c.h.append(k, k, c.ints([0, 2, 4, 6]), c.ints([30, 99, 64]), c.ints(c.table[:, :4]), max_new=2)
+    assert c.h.status() == H.HYB_STATUS_BAD_LENGTH
+    for b, start in ((0, 28), (2, 62)):
+        for x in "kv":
+            OP.append(c.codes[x], c.scales[x], f64(k[2 * b:2 * b + 2]).astype(np.float32), start, c.table[b], c.kind, c.page)
+    for x in "kv":
+        assert np.array_equal(c.t[x].view(c.torch.uint8).cpu().numpy(), c.codes[x]), x
+        assert np.array_equal(c.ts[x].cpu().numpy(), c.scales[x], equal_nan=True), x
+
+
 # ---- attention -----------------------------------------------------------------------------------------
 @pytest.mark.parametrize("kind,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("e4m3", "fp16"), ("int8", "fp16")])
 @pytest.mark.parametrize("d", [64, 128])
@@ -333,6 +391,68 @@ def test_attend_bad_lengths():
         assert c.torch.equal(full, got) and c.h.status(clear=True) == H.HYB_STATUS_BAD_LENGTH
         c.h.attend(q, c.ints([0, rows + 9, 1]), c.ints([64, -5]), t, max_new=rows, max_len=64)
         assert c.h.status(clear=True) & H.HYB_STATUS_BAD_LENGTH
+
+
+def check_positions(c, q, out, lse, pos, cap, window, n_sink):
+    """Each row against the oracle at the position it has; the others as they were.  The floor of the weights, 2^-31 max(vs)
+    sum |c| at most over 64 codes of up to 448, lies below 2^-20 of the largest value (a code of 100 or more times its scale)."""
+    sc = 1 / math.sqrt(c.d)
+    K, V = c.values(0, cap, "k"), c.values(0, cap, "v")
+    for i in range(q.shape[0]):
+        if i not in pos:
+            assert (out[i] == 7).all()
+            continue
+        t = pos[i]
+        gone = np.zeros(cap, bool)
+        if t < 0:
+            gone[:] = True
+        else:
+            gone |= np.arange(cap) > t
+            if window:
+                gone |= (np.arange(cap) <= t - window) & (np.arange(cap) >= n_sink)
+        ref, rl, mag, most = OP.attend(f64(q[i:i + 1]), K, V, 1, cap, sc, gone=gone)
+        e = (c.d + 16) * 2.0 ** -24 * most[..., None]
+        tol = HALF[c.dtype] * np.abs(ref) + (WEIGHT[c.dtype] + 2 * e + 2.0 ** -19) * mag + FLOOR[c.dtype] + 2.0 ** -20 * np.abs(V).max()
+        assert (np.abs(f64(out[i:i + 1]) - ref) <= tol).all(), i
+        assert np.array_equal(np.isneginf(f64(lse[i])), np.isneginf(rl[0]))
+        fin = np.isfinite(rl[0])
+        assert (np.abs(f64(lse[i])[fin] - rl[0][fin]) <= (e[0, :, 0] + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl[0]))[fin]).all()
+
+
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (5, 2), (20, 40), ((1 << 31) - 1, 0)])
+@pytest.mark.parametrize("G,dtype", [(1, "bf16"), (4, "bf16"), (16, "bf16"), (64, "bf16"), (16, "fp16"), (64, "fp16")])
+def test_attend_contradictions_move_no_row(window, n_sink, G, dtype):
+    """Rows past max_new are left as they were, rows before a sequence's begin see nothing, rows past the table see what is
+    in it, and the status is set, for every number of rows a KV head (and so every form)."""
+    import hybrid_sparse_linear_decode_b200 as H
+    c = Paged([64], 16, 1, 64, dtype=dtype, seed=25)
+    table = c.ints(c.table[:, :4])
+    for cu, lens, rows, max_new, _ in CONTRADICTIONS:
+        first = max(cu[0], 0)
+        n = max(0, min(cu[1], rows) - first, 0)
+        pos = {first + i: lens[0] - cu[1] + first + i for i in range(min(n, max_new))}
+        q = c.rows(rows, G)
+        out = c.torch.full_like(q, 7.0)
+        got, lse = c.h.attend(q, c.ints(cu), c.ints(lens), table, max_new, 64, window=window, n_sink=n_sink, out=out, return_lse=True)
+        assert c.h.status(clear=True) == H.HYB_STATUS_BAD_LENGTH, (cu, lens)
+        check_positions(c, q, out, lse, pos, 64, window, n_sink)
+
+
+@pytest.mark.parametrize("new,length", [(1, 9000), (9, 9000), (2, 9000), (40, 9000)])
+def test_attend_status_of_sequences_without_work(new, length):
+    """A contradiction is told where its sequence has nothing to do, too: beside long sequences, which go by the line."""
+    import hybrid_sparse_linear_decode_b200 as H
+    for B in (2, 40):
+        lens = [length] + [16] * (B - 1)
+        c = Paged(lens, 64, 1, 64, "int8", seed=26)
+        cu = np.full(B + 1, new, np.int32)
+        cu[0] = 0
+        for bad in (1, B - 1):
+            worse = list(lens)
+            worse[bad] = -1
+            for ls, want in ((lens, 0), (worse, H.HYB_STATUS_BAD_LENGTH)):
+                c.h.attend(c.rows(new, 4), c.ints(cu), c.ints(ls), c.ints(c.table), new, length)
+                assert c.h.status(clear=True) == want
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])

@@ -11,9 +11,10 @@ namespace {
 // Codes become f16 exactly.  Query rows are divided by a power of two that puts
 // their largest element in [1, 2), so bf16 queries become f16 with no loss above
 // 2^-17 of that element.  Weights are stored as f16(2^(z - m + 15) vs / ref) with
-// ref a power of two that is at least every scale so far: at most 2^15, and full
-// 11 bits down to 2^-29 of the largest, which is one rounding of 2^-12 a weight,
-// below the output type's own.  All sums are in 32 bits.
+// ref a power of two that is at least every scale that the row has seen so far: at most
+// 2^15, and full 11 bits down to 2^-29 of the largest, which is one rounding of 2^-12 a
+// weight, below the output type's own.  Each row has a ref of its own: a scale of pages that
+// other rows of its tile see, and it does not, has no part in it.  All sums are in 32 bits.
 //
 // Matrix form (mma.m16n8k16), with 8 query rows as the narrow side so that the few
 // rows of a decode step fill it: S^T = C_k Q^T with 16 tokens by 8 rows, O^T = C_v^T P^T
@@ -134,12 +135,11 @@ template <int D, int NT>
 struct Rows {
   float o[NT][D / 16][4];  // channels (D / 8) g + 2 j (elements 0, 1) and the next (2, 3), g = lane / 4
   float m[NT][2], l[NT][2], rf[NT][2];
+  float inv[NT][2];      // 1 / the value scales' reference, a power of two
   int pos[NT][2];        // position, or -1 for a row that is not there or lies before its sequence
-  uint32_t ref;          // exponent field of the value scales' reference
   int pos_min, pos_max;  // of the warp's rows that are there
 
   __device__ __forceinline__ void clear() {
-    ref = 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -147,6 +147,7 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
       m[n][0] = m[n][1] = -INFINITY;
+      inv[n][0] = inv[n][1] = pow2_of(253);
       l[n][0] = l[n][1] = 0.f;
     }
   }
@@ -267,34 +268,47 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
   // Logits, and whether one passes its row's running maximum.  A stage that every row sees whole needs no mask.
   const bool whole = live.x == 16 && live.y == 16 && base + kStageTokens <= R.pos_min + 1 &&
                      (p.W == 0 || base > R.pos_max - p.W || base + kStageTokens <= p.S);
+  float v[2][NT][2];  // value scales over the rows' references; 0 where a row sees none of the 16 tokens
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float f = (i ? sc.y : sc.x) * R.rf[n][c];
+        v[i][n][c] = (i ? sc.w : sc.z) * R.inv[n][c];
+        s[i][n][c] *= f;
+        s[i][n][2 + c] *= f;
+      }
+  if (!whole) {  // a block of its own: 8 drafts of 8 sequences of up to 32768 162 us, with selects in the loop above 177
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int first = base + 16 * i, there = i ? live.y : live.x;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int pos = R.pos[n][c];
+          if (there <= 0 || first > pos || (p.W > 0 && first + there - 1 <= pos - p.W && first >= p.S)) v[i][n][c] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int in = g + 8 * e, tok = first + in;
+            const bool seen = in < there && tok <= pos && (p.W == 0 || tok > pos - p.W || tok < p.S);
+            if (!seen) s[i][n][2 * e + c] = -INFINITY;
+          }
+        }
+    }
+  }
   float top[NT][2];
   bool moved = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      top[n][c] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f = (i ? sc.y : sc.x) * R.rf[n][c];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float z = s[i][n][2 * e + c] * f;
-          if (!whole) {
-            const int in = g + 8 * e, tok = base + 16 * i + in, pos = R.pos[n][c];
-            const bool seen = in < (i ? live.y : live.x) && tok <= pos && (p.W == 0 || tok > pos - p.W || tok < p.S);
-            z = seen ? z : -INFINITY;
-          }
-          s[i][n][2 * e + c] = z;
-          top[n][c] = fmaxf(top[n][c], z);
-        }
-      }
-      moved |= top[n][c] > R.m[n][c];
+      top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+      moved |= top[n][c] > R.m[n][c] || fmaxf(v[0][n][c], v[1][n][c]) > 1.f;
     }
-  const uint32_t ref = max(R.ref, max(pow2_above(sc.z), pow2_above(sc.w)));
-  if (__any_sync(0xffffffffu, moved || ref != R.ref)) {
-    const float down = pow2_of(R.ref) * pow2_of(254u - ref);
-    R.ref = ref;
+  if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
@@ -308,7 +322,15 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
         f[c] = m == R.m[n][c] ? 1.f : exp2_fast(R.m[n][c] - m);  // 0 where no token was seen before
         R.m[n][c] = m;
         R.l[n][c] *= f[c];
-        f[c] *= down;
+        // a reference is at least every scale that the row sees
+        const float was = R.inv[n][c];
+        uint32_t ref = 254u - (__float_as_uint(was) >> 23);
+        if (v[0][n][c] > 1.f) ref = max(ref, pow2_above(sc.z));
+        if (v[1][n][c] > 1.f) ref = max(ref, pow2_above(sc.w));
+        R.inv[n][c] = pow2_of(254u - ref);
+        f[c] *= pow2_inverse(was) * R.inv[n][c];
+        if (v[0][n][c] != 0.f) v[0][n][c] = sc.z * R.inv[n][c];
+        if (v[1][n][c] != 0.f) v[1][n][c] = sc.w * R.inv[n][c];
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
@@ -320,7 +342,6 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
     }
   }
   // Weights, rounded and transposed: b[i][n] are tokens 2 t, 2 t + 1 (and 8 more) of tile i for row g
-  const float v0 = sc.z * pow2_of(254u - ref), v1 = sc.w * pow2_of(254u - ref);
   uint32_t b[2][NT][2], fine[FINE ? 2 : 1][FINE ? NT : 1][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -328,13 +349,12 @@ __device__ __forceinline__ void do_stage(const PagedAttnParams& p, const uint8_t
     const float m0 = R.m[n][0] == -INFINITY ? 0.f : R.m[n][0] - 15.f, m1 = R.m[n][1] == -INFINITY ? 0.f : R.m[n][1] - 15.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float v = i ? v1 : v0;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float w0 = exp2_fast(s[i][n][2 * e] - m0), w1 = exp2_fast(s[i][n][2 * e + 1] - m1);
         R.l[n][0] += w0;
         R.l[n][1] += w1;
-        const float u0 = w0 * v, u1 = w1 * v;
+        const float u0 = w0 * v[i][n][0], u1 = w1 * v[i][n][1];
         const uint32_t r = pack_half(u0, u1);
         b[i][n][e] = transpose8(r);
         if (FINE) {
@@ -550,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
       for (int c = 0; c < 2; ++c) {
         float* e = body + (team * kRows + 8 * (NT * member + n) + 2 * t + c) * kRowFloats;
         put_row<D, NT>(R, n, c, 1.f, e);
-        if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c], e[D + 2] = pow2_of(R.ref);
+        if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c], e[D + 2] = pow2_inverse(R.inv[n][c]);
       }
     __syncthreads();
     for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
@@ -843,7 +863,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float* e = body + (2 * t + c) * kRowFloats;
-      put_row<D, NT>(R, n, c, R.l[n][c] == 0.f ? 0.f : pow2_of(R.ref) / R.l[n][c], e);
+      put_row<D, NT>(R, n, c, R.l[n][c] == 0.f ? 0.f : pow2_inverse(R.inv[n][c]) / R.l[n][c], e);
       if (g == 0) e[D] = R.m[n][c], e[D + 1] = R.l[n][c];
     }
     __syncwarp();

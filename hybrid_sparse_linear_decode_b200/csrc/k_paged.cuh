@@ -87,6 +87,8 @@ __device__ __forceinline__ uint32_t pow2_above(float x) {
   return min(max((u >> 23) + ((u & 0x7fffffu) ? 1u : 0u), 1u), 253u);
 }
 __device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
+// 1 / x of a power of two x from 2^-126 to 2^126.
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // ---- what a row tile sees -------------------------------------------------------------------------
 // Where the visible tokens of a row tile lie: sinks [0, sink), then [lo, hi)

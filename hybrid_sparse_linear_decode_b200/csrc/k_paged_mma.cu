@@ -8,7 +8,8 @@
 //     O [128 x D] in tensor memory).
 // Within a CTA the products and the softmax of a tile follow one another; two CTAs share an SM, and the one's softmax
 // runs beside the other's products.  A row's maximum is followed only when a tile passes it by more than 2^8, so O is
-// rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest.
+// rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest; ref is
+// a row's own, from the scales of what it sees.
 //
 // 2047 tokens of 10001, 32 heads of 128: 606 us, 497 TFLOP/s.  Bound by the chain of a tile: the operands' way from shared
 // memory and the conversions into it (about 2000 clocks a tile) beside a softmax of about 3400.  Tiles of 64 tokens with two
@@ -328,10 +329,6 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
         if (any && alive) {
           const float* sc = reinterpret_cast<const float*>(smem + Geo::kScales) + (t & 1) * 2 * kGroups;
           const int* live = reinterpret_cast<const int*>(smem + Geo::kLive) + (t & 1) * kGroups;
-          uint32_t now = ref;
-#pragma unroll
-          for (int i = 0; i < kGroups; ++i) now = max(now, pow2_above(sc[kGroups + i]));
-          const float down = pow2_of(254u - now);
           // which of 32 tokens the row sees
           auto seen = [&](int c) {
             const int at = base + 32 * c;
@@ -341,18 +338,20 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
           };
           // The tile's maximum.  Loops are not unrolled: a warp alone on its scheduler runs straight code at the rate
           // at which it is fetched.
-          float top = -INFINITY;
+          float top = -INFINITY, most = 0.f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t r[32];
             tmem_load(mine + 32 * c, r);
             const uint32_t see = seen(c);
             const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+            float v0 = sc[kGroups + 2 * c], v1 = sc[kGroups + 2 * c + 1];
             tmem_wait_load();
             float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (!all) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = (see >> i) & 1u ? r[i] : 0xff800000u;
+              v0 = see & 0xffffu ? v0 : 0.f, v1 = see >> 16 ? v1 : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -360,10 +359,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
               for (int e = 0; e < 2; ++e)
                 u[2 * (i / 16) + e] = fmaxf(u[2 * (i / 16) + e], fmaxf(__uint_as_float(r[i + 2 * e]), __uint_as_float(r[i + 2 * e + 1])));
             // scales are not negative, so the largest product gives the largest logit
+            most = fmaxf(most, fmaxf(v0, v1));
             const float u0 = fmaxf(u[0], u[1]), u1 = fmaxf(u[2], u[3]);
             top = fmaxf(top, u0 == -INFINITY ? -INFINITY : u0 * (sc[2 * c] * rf));
             top = fmaxf(top, u1 == -INFINITY ? -INFINITY : u1 * (sc[2 * c + 1] * rf));
           }
+          const uint32_t now = max(ref, pow2_above(most));
+          const float down = pow2_of(254u - now);
           const bool grown = m == -INFINITY ? top > m : top > m + kGrowth;
           if (__any_sync(0xffffffffu, grown || now != ref)) {
             const float mn = grown ? top : m;
@@ -391,7 +393,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
             tmem_load(mine + 32 * c, r);
             const uint32_t see = seen(c);
             const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
-            const float f0 = sc[2 * c] * rf, f1 = sc[2 * c + 1] * rf, v0 = sc[kGroups + 2 * c] * down, v1 = sc[kGroups + 2 * c + 1] * down;
+            const float f0 = sc[2 * c] * rf, f1 = sc[2 * c + 1] * rf, v0 = all || (see & 0xffffu) ? sc[kGroups + 2 * c] * down : 0.f, v1 = all || (see >> 16) ? sc[kGroups + 2 * c + 1] * down : 0.f;
             float2 add = make_float2(0.f, 0.f);
             const float2 nn = make_float2(shift, shift);
             tmem_wait_load();

@@ -393,11 +393,14 @@ def test_attend_bad_lengths():
         assert c.h.status(clear=True) & H.HYB_STATUS_BAD_LENGTH
 
 
-def check_positions(c, q, out, lse, pos, cap, window, n_sink):
-    """Each row against the oracle at the position it has; the others as they were.  The floor of the weights, 2^-31 max(vs)
-    sum |c| at most over 64 codes of up to 448, lies below 2^-20 of the largest value (a code of 100 or more times its scale)."""
+def check_positions(c, q, out, lse, pos, cap, window, n_sink, step=2.0 ** -31):
+    """Each row against the oracle at the position it has; the others as they were.  The floor of the weights is the
+    row's own: `step` times the largest value scale that it sees, for each code that it sees.  A weight is stored as f16
+    2^15 times itself (tcgen05: 2^7 at least), in units of a power of two below twice that scale, so one below 2^-14 there is
+    rounded to multiples of 2^-24: half a step is 2^-40 (2^-32) of these units."""
     sc = 1 / math.sqrt(c.d)
     K, V = c.values(0, cap, "k"), c.values(0, cap, "v")
+    scale = c.scales["v"][c.table[0, :cap // c.page]].astype(np.float64).repeat(c.page, 0)[..., None]   # of each token
     for i in range(q.shape[0]):
         if i not in pos:
             assert (out[i] == 7).all()
@@ -412,7 +415,8 @@ def check_positions(c, q, out, lse, pos, cap, window, n_sink):
                 gone |= (np.arange(cap) <= t - window) & (np.arange(cap) >= n_sink)
         ref, rl, mag, most = OP.attend(f64(q[i:i + 1]), K, V, 1, cap, sc, gone=gone)
         e = (c.d + 16) * 2.0 ** -24 * most[..., None]
-        tol = HALF[c.dtype] * np.abs(ref) + (WEIGHT[c.dtype] + 2 * e + 2.0 ** -19) * mag + FLOOR[c.dtype] + 2.0 ** -20 * np.abs(V).max()
+        low = step * (scale[~gone].max(0) * np.abs(V[~gone] / scale[~gone]).sum(0)) if (~gone).any() else np.zeros(V.shape[1:])
+        tol = HALF[c.dtype] * np.abs(ref) + (WEIGHT[c.dtype] + 2 * e + 2.0 ** -19) * mag + FLOOR[c.dtype] + np.repeat(low, q.shape[1] // c.Hkv, 0)
         assert (np.abs(f64(out[i:i + 1]) - ref) <= tol).all(), i
         assert np.array_equal(np.isneginf(f64(lse[i])), np.isneginf(rl[0]))
         fin = np.isfinite(rl[0])
@@ -453,6 +457,37 @@ def test_attend_status_of_sequences_without_work(new, length):
             for ls, want in ((lens, 0), (worse, H.HYB_STATUS_BAD_LENGTH)):
                 c.h.attend(c.rows(new, 4), c.ints(cu), c.ints(ls), c.ints(c.table), new, length)
                 assert c.h.status(clear=True) == want
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,G,new,step", [("bf16", 1, 4, 2.0 ** -39), ("bf16", 4, 4, 2.0 ** -39), ("fp16", 2, 15, 2.0 ** -39),
+                                              ("bf16", 4, 20, 2.0 ** -31), ("bf16", 16, 20, 2.0 ** -31), ("fp16", 16, 20, 2.0 ** -39)])
+@pytest.mark.parametrize("times", [2.0 ** 24, 2.0 ** 30, 2.0 ** 36, 2.0 ** 60, np.inf, np.nan])
+def test_attend_scales_of_pages_a_row_does_not_see(kind, dtype, G, new, step, times):
+    """Value scales far larger on a page that only later rows see, or only earlier ones (behind the others' window): each
+    row's weights keep their bits whatever it does not see."""
+    import hybrid_sparse_linear_decode_b200 as H
+    for page, length, window in ((3, 48 + new // 2, 0), (0, 31 + new // 2, 16)):
+        c = Paged([length], 16, 2, 64, kind, dtype, seed=27)
+        pid = c.table[0, page]
+        for x in "kv":
+            c.scales[x][c.table[0, :4]] = 2.0 ** -7       # all alike but for that page
+        c.scales["v"][pid] *= np.float32(times)
+        if not np.isfinite(times):
+            c.scales["k"][pid] = times
+        for x in "kv":
+            c.ts[x].copy_(c.torch.from_numpy(c.scales[x]))
+        sees = (lambda t: t >= 48) if page else (lambda t: t - window < 15)
+        first = length - new
+        assert 0 < sum(sees(first + i) for i in range(new)) < new
+        q = c.rows(new, 2 * G)
+        out, lse = c.h.attend(q, c.ints([0, new]), c.ints([length]), c.ints(c.table), new, length, window=window, return_lse=True)
+        rows = [i for i in range(new) if np.isfinite(times) or not sees(first + i)]
+        if not np.isfinite(times):
+            c.scales["k"][pid] = c.scales["v"][pid] = 1.0    # for the oracle, whose rows do not see it either
+        if dtype == "fp16":     # whose results end at 65504
+            rows = [i for i in rows if not sees(first + i)]
+        check_positions(c, q[rows], out[rows], lse[rows], {j: first + i for j, i in enumerate(rows)}, 16 * -(-length // 16), window, 0, step)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])

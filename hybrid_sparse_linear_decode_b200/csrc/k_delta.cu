@@ -144,9 +144,11 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
 //
 // Operands are f16.  Rows of K and Q are divided by powers of two kappa that put their largest element in [1, 2), so
 // they go in exactly (but for elements below 2^-17 of it); S, W, T and the U that the state takes as two f16 parts, 22
-// bits, after S and W are divided by powers of two of each column of the state (sigma, omega), so that values of any
-// size keep them.  Only O, whose result has 8 bits, takes single parts of S, U and P.  Sums are in 32 bits.  Errors of
-// the state stay near those of 32-bit arithmetic.
+// bits, after S and W are divided by powers of two of each column of the state (sigma, omega), so that columns keep them
+// whose largest value is 2^-119 or more.  (W is formed in units of tau, sigma but at least 1, so that V divided by it
+// stays finite beside a state of any smallness: 2 us of 705 below; a branch around it for states of ordinary size takes 8.)
+// Only O, whose result has 8 bits, takes single parts of S, U and P.
+// Sums are in 32 bits.  Errors of the state stay near those of 32-bit arithmetic.
 //
 // What bounds it: the chain from chunk to chunk and the instructions of both sides.  32 heads of 128 x 128 and 8192
 // tokens: 700 us, 10400 clocks a chunk; the scanning warps alone 7300 (their products 1600), the preparing ones alone
@@ -518,7 +520,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     return __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), halves);
   };
   bool alive = true, ok = true;
-  float unit = 1.f, sig = 1.f, om = 1.f;
+  float unit = 1.f, sig = 1.f, wun = 1.f;  // units of the state, of its halves, of U
   const uint32_t my_s = mine + kColS + h * kKeys;
 #pragma unroll 1
   for (int i = 0; i < kKeys; i += 32) {
@@ -548,7 +550,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int at = i + 2 * e;
-          const float2 y = fma2(mul2(pair(q[at], q[at + 1]), both(sig)), dd[e], mul2(mul2(pair(u[at], u[at + 1]), both(sig * om)), oo[e]));
+          const float2 y = fma2(mul2(pair(q[at], q[at + 1]), both(sig)), dd[e], mul2(mul2(pair(u[at], u[at + 1]), both(wun)), oo[e]));
           u[at / 2] = pack_bf16(y.x, y.y);
         }
       }
@@ -590,7 +592,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     most_s[128 * h + row] = top;
     bar_sync(2, 256);
     top = fmaxf(top, most_s[128 * (1 - h) + row]);
-    s = pow2_of(field_of(top * unit, 127 - 30, 127 + 110) - 6);
+    s = pow2_of(field_of(top * unit, 8, 253) - 6);
     {
       const float f = fminf(unit * pow2_inverse(s), FLT_MAX);
 #pragma unroll
@@ -640,7 +642,8 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     uint32_t x[32];
     tmem_load(mine + kColX + 32 * h, x);
     tmem_wait_load();
-    const float inv = pow2_inverse(sig);
+    const float tau = fmaxf(sig, 1.f), inv = pow2_inverse(tau);
+    const float2 to_tau = both(sig * inv);
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -649,7 +652,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t two = swap(v[i / 2 + e]);
-        const float2 y = fma2(pair(x[i + 2 * e], x[i + 2 * e + 1]), ff[e], mul2(mul2(make_float2(bf16_lo(two), bf16_hi(two)), both(inv)), ww[e]));
+        const float2 y = fma2(mul2(pair(x[i + 2 * e], x[i + 2 * e + 1]), to_tau), ff[e], mul2(mul2(make_float2(bf16_lo(two), bf16_hi(two)), both(inv)), ww[e]));
         x[i + 2 * e] = __float_as_uint(y.x), x[i + 2 * e + 1] = __float_as_uint(y.y);
         most = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), most);
       }
@@ -657,7 +660,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     most_w[128 * h + row] = most;
     bar_sync(2, 256);
     most = fmaxf(most, most_w[128 * (1 - h) + row]);
-    om = pow2_of(field_of(most, 127 - 60, 127 + 96) - 6);
+    const float om = pow2_of(field_of(most, 8, 253) - 6);
     const float back = pow2_inverse(om);
     {
       uint32_t hi[16], lo[16];
@@ -687,8 +690,8 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     __syncwarp();
     // The state's new unit is the larger of its decayed part's and of U's; meanwhile it decays.
     const float whole = E[kWhole * kC - 32 * h];
-    om *= E[kWhole * kC - 32 * h + 1];  // U goes on times kappa
-    const float now = fminf(fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), sig * om), pow2_of(27)), pow2_of(253));
+    wun = tau * (om * E[kWhole * kC - 32 * h + 1]);  // U goes on times kappa
+    const float now = fminf(fmaxf(fmaxf(sig * pow2_of(field_of(whole, 1, 127)), wun), pow2_of(8)), pow2_of(253));
     const float by = pow2_inverse(now);
     {
       const float f = whole * fminf(unit * by, FLT_MAX);
@@ -711,7 +714,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
     tmem_load(mine + kColX + 32 * h, x);
     tmem_wait_load();
     {
-      const float part = sig * om * by;
+      const float part = wun * by;
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {

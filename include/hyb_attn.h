@@ -556,6 +556,8 @@ typedef struct hyb_attn_delta_state {
  *          all;  beta the learning rate.  k is taken as it is: for the rule to be
  *          stable |k| <= 1 and 0 <= beta <= 1 (or beta |k|^2 < 2).  Values are
  *          finite: one that is not spoils its sequence's head from up to 63 tokens before.
+ *          In chunks errors are relative to the largest element of a column of the state
+ *          within a chunk, or to 2^-119 where that is larger.
  *   out    bf16 rows of [n_v_heads][value_dim], in other memory than the inputs
  * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
  * the tokens one by one with the state in registers; long ones in chunks of 64

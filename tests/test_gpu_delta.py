@@ -118,6 +118,43 @@ def test_delta_sizes_of_values(new, size):
     Delta(new, 1, 2, 128, 64, seed=3, size=size).check()
 
 
+@pytest.mark.parametrize("new", [[5, 4], [13], [14], [100, 130]])
+@pytest.mark.parametrize("size", [1e-20, 1e-28, 1e-33])
+def test_delta_small_states(new, size):
+    """Values far below 1, tokens one by one and in chunks: with values of their size, and read and rewritten with none."""
+    Delta(new, 1, 2, 128, 64, seed=3, size=size).check()
+    d = Delta(new, 1, 2, 64, 128, seed=13, size=size)
+    d.v.zero_()
+    d.check()
+    d.beta.zero_()
+    d.check()
+
+
+@pytest.mark.parametrize("new", [[13], [14], [150]])
+def test_delta_columns_of_different_sizes(new):
+    """With no values a state's columns do not meet: each keeps its own precision, whatever its size."""
+    d = Delta(new, 1, 2, 128, 128, seed=14)
+    d.v.zero_()
+    size = 10.0 ** -np.linspace(-20, 33, 128)
+    d.state *= d.torch.from_numpy(size).cuda().float()
+    S0, (q, k, v, g, beta) = f64(d.state), (f64(x) for x in (d.q, d.k, d.v, d.g, d.beta))
+    out = f64(d.h.run(d.q, d.k, d.v, d.g, d.beta, d.ints(d.cu), max_new=max(new)))
+    ref, want, mag = OD.run(S0[0], q, k, v, g, beta, 1 / math.sqrt(128))
+    rel = 8 * math.sqrt(new[0] * 128) * 2.0 ** -24
+    inn = np.linalg.norm(S0[0], axis=1)
+    assert (np.linalg.norm(f64(d.state)[0] - want, axis=1) <= rel * inn).all()
+    assert (np.abs(out - ref) <= 2.0 ** -8 * np.abs(ref) + 3 * 2.0 ** -11 * mag + rel * inn / math.sqrt(128)).all()
+
+
+@pytest.mark.parametrize("new", [[13], [14], [150]])
+@pytest.mark.parametrize("size,values", [(1e-30, 1.0), (1e-30, 1e15), (1e-12, 1e18), (1e-37, 1e-30), (0.0, 1e33), (1e20, 1e33),
+                                         (0.0, 1e-33)])
+def test_delta_values_far_above_the_state(new, size, values):
+    d = Delta(new, 1, 2, 64, 64, seed=15, size=values)
+    d.state *= size / values
+    d.check()
+
+
 @pytest.mark.parametrize("new", [[5, 4], [64], [100, 130]])
 @pytest.mark.parametrize("keys", [2.0 ** -8, 2.0 ** -14, 2.0 ** -30])
 def test_delta_short_keys(new, keys):

@@ -1,4 +1,7 @@
 // The gated delta rule: S := a S, S := S + k (beta (v - S^T k))^T, o = scale S^T q, a = exp(g).
+//
+// The kernels start before the one before them on the stream has ended (and wait for it before they read anything), so
+// what they read may still be written while they run: plain loads only, none by the path of read-only data.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,7 +50,7 @@ struct Piece {
   uint4 w[DK / 32];  // DK / 4 bf16 in a row
   __device__ __forceinline__ void load(const uint16_t* p) {
 #pragma unroll
-    for (int i = 0; i < DK / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < DK / 32; ++i) w[i] = *(reinterpret_cast<const uint4*>(p) + i);
   }
   __device__ __forceinline__ float at(int i) const {
     const uint4& u = w[i / 8];
@@ -76,9 +79,9 @@ __global__ void __launch_bounds__(128) delta_steps_kernel(const DeltaParams p) {
   auto fetch = [&](int t) {
     k.load(p.k + (int64_t)t * p.k_stride + (int64_t)hk * DK + row0);
     q.load(p.q + (int64_t)t * p.q_stride + (int64_t)hk * DK + row0);
-    v = __ldg(reinterpret_cast<const uint2*>(p.v + (int64_t)t * p.v_stride + (int64_t)hv * p.DV + col));
-    g = __ldg(p.g + (int64_t)t * p.Hv + hv);
-    beta = __ldg(p.beta + (int64_t)t * p.Hv + hv);
+    v = *reinterpret_cast<const uint2*>(p.v + (int64_t)t * p.v_stride + (int64_t)hv * p.DV + col);
+    g = p.g[(int64_t)t * p.Hv + hv];
+    beta = p.beta[(int64_t)t * p.Hv + hv];
   };
   fetch(r.t0);
   for (int t = r.t0; t < r.t0 + r.n; ++t) {
@@ -223,7 +226,7 @@ __device__ __forceinline__ void load_rows(uint4 (&w)[4], const uint16_t* src, in
   src += r * stride + tid % kPieces * 8;
 #pragma unroll
   for (int i = 0; i < 4; ++i, r += kStep, src += kStep * stride)
-    w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    w[i] = r < n ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
 }
 template <int DK>
 __device__ __forceinline__ void store_rows(const uint4 (&w)[4], uint8_t* tile, float* kappa, int first, int tid) {
@@ -270,8 +273,8 @@ __device__ __forceinline__ void begin_chunk(const DeltaParams& p, Ahead& a, int 
   if (tid >= 96) {
     const int r0 = 2 * (tid - 96), r1 = r0 + 1;
     const int64_t at = (int64_t)(row + r0) * p.Hv + hv;
-    a.g0 = r0 < n ? __ldg(p.g + at) : 0.f, a.g1 = r1 < n ? __ldg(p.g + at + p.Hv) : 0.f;
-    a.b0 = r0 < n ? __ldg(p.beta + at) : 0.f, a.b1 = r1 < n ? __ldg(p.beta + at + p.Hv) : 0.f;
+    a.g0 = r0 < n ? p.g[at] : 0.f, a.g1 = r1 < n ? p.g[at + p.Hv] : 0.f;
+    a.b0 = r0 < n ? p.beta[at] : 0.f, a.b1 = r1 < n ? p.beta[at + p.Hv] : 0.f;
   }
 }
 
@@ -611,7 +614,7 @@ __device__ __forceinline__ void scan_chunks(const DeltaParams& p, uint8_t* smem,
       const uint16_t* from = v0 + (int64_t)(c * kC) * p.v_stride;
       const int64_t step = 2 * p.v_stride;
 #pragma unroll
-      for (int i = 0; i < 16; ++i, from += step) v[i] = 2 * i < n ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+      for (int i = 0; i < 16; ++i, from += step) v[i] = 2 * i < n ? *reinterpret_cast<const uint32_t*>(from) : 0u;
     }
     tmem_wait_store();
     fence_before();

@@ -78,8 +78,8 @@ __device__ __forceinline__ StagePages stage_pages(const PagedAttnParams& p, cons
   const int P = p.c.P;
   const uint32_t a = (uint32_t)base >> 4, b = a + 1;
   const int ia = P == 16 ? (int)a : (int)__umulhi(a, magic), ib = P == 16 ? (int)b : (int)__umulhi(b, magic);
-  g.p0 = base < end ? __ldg(table + ia) : -1;
-  g.p1 = base + 16 < end ? __ldg(table + ib) : -1;
+  g.p0 = base < end ? table[ia] : -1;
+  g.p1 = base + 16 < end ? table[ib] : -1;
   g.o0 = base - ia * P;
   g.o1 = base + 16 - ib * P;
   if ((base < end && (uint32_t)g.p0 >= (uint32_t)p.c.n_pages) ||
@@ -178,7 +178,7 @@ __device__ __forceinline__ void fetch_rows(const PagedAttnParams& p, RawRows<D, 
     for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        raw.z[n][hh][e] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * hh) + e) : make_uint4(0, 0, 0, 0);
+        raw.z[n][hh][e] = there ? *(reinterpret_cast<const uint4*>(src + 64 * hh) + e) : make_uint4(0, 0, 0, 0);
   }
 }
 // Their fragments, factors and positions.

@@ -1,4 +1,7 @@
 // Device helpers shared by the kernels of the paged 8-bit cache.
+//
+// These kernels start before the one before them on the stream has ended (and wait for it before they read anything), so
+// what they read may still be written while they run: plain loads only, none by the path of read-only data.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -85,7 +85,7 @@ struct Raw {
   uint4 a, b;
 };
 __device__ __forceinline__ Raw load_runs(const uint16_t* row, const Runs& r) {
-  return Raw{__ldg(reinterpret_cast<const uint4*>(row + r.c0)), __ldg(reinterpret_cast<const uint4*>(row + r.c1))};
+  return Raw{*reinterpret_cast<const uint4*>(row + r.c0), *reinterpret_cast<const uint4*>(row + r.c1)};
 }
 __device__ __forceinline__ void to_values(const Raw& raw, bool half, float* x) {
   const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
@@ -101,7 +101,7 @@ struct Angles {
 __device__ __forceinline__ void load_angles(Angles& a, const float* row, int rot, int at) {
   const float4* c = reinterpret_cast<const float4*>(row + at);
   const float4* s = reinterpret_cast<const float4*>(row + rot / 2 + at);
-  const float4 x = __ldg(c), y = __ldg(c + 1), z = __ldg(s), w = __ldg(s + 1);
+  const float4 x = c[0], y = c[1], z = s[0], w = s[1];
   a.c[0] = x.x, a.c[1] = x.y, a.c[2] = x.z, a.c[3] = x.w, a.c[4] = y.x, a.c[5] = y.y, a.c[6] = y.z, a.c[7] = y.w;
   a.s[0] = z.x, a.s[1] = z.y, a.s[2] = z.z, a.s[3] = z.w, a.s[4] = w.x, a.s[5] = w.y, a.s[6] = w.z, a.s[7] = w.w;
 }

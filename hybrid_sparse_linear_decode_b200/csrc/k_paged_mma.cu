@@ -124,7 +124,7 @@ struct Pieces {
 // The table's entry for the group of 16 tokens that begins at tok, -1 past the end.
 __device__ __forceinline__ int entry_of(const PagedAttnParams& p, const int32_t* table, int tok, int end, uint32_t magic) {
   const uint32_t g = (uint32_t)tok >> 4;
-  return tok < end ? __ldg(table + (p.c.P == 16 ? g : __umulhi(g, magic))) : -1;
+  return tok < end ? table[p.c.P == 16 ? g : __umulhi(g, magic)] : -1;
 }
 template <bool INT8>
 __device__ __forceinline__ void convert_piece(const uint4& c, uint4& lo, uint4& hi) {
@@ -192,7 +192,7 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
     auto load = [&](const uint8_t* codes, uint4 (&to)[kN]) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        to[i] = from[i] != kNone ? __ldg(reinterpret_cast<const uint4*>(codes) + from[i]) : make_uint4(0, 0, 0, 0);
+        to[i] = from[i] != kNone ? *(reinterpret_cast<const uint4*>(codes) + from[i]) : make_uint4(0, 0, 0, 0);
     };
     auto load_scales = [&]() {
       ks = vs = 0.f;
@@ -200,8 +200,8 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
       if (tid < kGroups && base + 16 * tid < end && (uint32_t)gpage >= (uint32_t)p.c.n_pages) {
         raise(p.status, HYB_STATUS_BAD_PAGE);
       } else if (tid < kGroups && base + 16 * tid < end) {
-        ks = __ldg(p.c.ks + (int64_t)gpage * p.c.Hkv + x.h);
-        vs = __ldg(p.c.vs + (int64_t)gpage * p.c.Hkv + x.h);
+        ks = p.c.ks[(int64_t)gpage * p.c.Hkv + x.h];
+        vs = p.c.vs[(int64_t)gpage * p.c.Hkv + x.h];
         live = min(max(end - base - 16 * tid, 0), 16);
       }
     };
@@ -293,7 +293,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          z[i] = there ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+          z[i] = there ? *(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(in_lo(u[e], half)), fabsf(in_hi(u[e], half))));

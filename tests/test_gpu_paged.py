@@ -217,6 +217,41 @@ def test_append_queries_in_place_and_strided():
     check_append(c, [1, 25], [8, 5], rot=64, interleaved=True, Hq=7, wide=3, inplace=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 5, 60])
+def test_rotation_in_place_then_attention(new, dtype):
+    """Steps one behind the other on the stream, nothing between them, whose queries are rotated where they lie, in a buffer
+    that the next step uses again: the same as step by step with waits and buffers of their own."""
+    import torch
+    import hybrid_sparse_linear_decode_b200 as H
+    steps = 12
+    c, e = (Paged([0, 0], 16, 2, 128, "e4m3", dtype, seed=28) for _ in "ab")
+    table = c.ints(c.rng.permutation(2 * 64).reshape(2, 64))
+    for x in (c, e):
+        x.h = H.PagedKVCache(128, 16, 2, 128)
+    rope = angles(1024, 128)
+    cu = c.ints([0, new, 2 * new])
+    rows = [[c.rows(2 * new, h) for h in (8, 2, 2)] for _ in range(steps)]
+    lens = [c.ints([new * (i + 1)] * 2) for i in range(steps)]
+    want = []
+    for (q, k, v), n in zip(rows, lens):
+        turned = e.h.append(k, v, cu, n, table, max_new=new, rope=rope, q=q)
+        torch.cuda.synchronize()
+        want.append(e.h.attend(turned, cu, n, table, new, 1024).clone())
+        torch.cuda.synchronize()
+    got = [torch.empty_like(w) for w in want]
+    bq, bk, bv = (torch.empty_like(x) for x in rows[0])
+    for (q, k, v), n, out in zip(rows, lens, got):
+        bq.copy_(q), bk.copy_(k), bv.copy_(v)
+        c.h.append(bk, bv, cu, n, table, max_new=new, rope=rope, q=bq, q_out=bq)
+        c.h.attend(bq, cu, n, table, new, 1024, out=out)
+    torch.cuda.synchronize()
+    assert c.h.status() == 0 and e.h.status() == 0
+    for i in range(steps):
+        assert torch.equal(got[i], want[i]), i
+    assert torch.equal(c.h.k_pages.view(torch.uint8), e.h.k_pages.view(torch.uint8)) and torch.equal(c.h.v_scales, e.h.v_scales)
+
+
 def test_append_extremes():
     """Zeros, values far below and above a code's range, infinities and NaN: stored as the header says."""
     import torch

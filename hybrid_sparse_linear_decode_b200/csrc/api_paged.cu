@@ -29,6 +29,8 @@ bool shapes_ok(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b) {
   if (c->head_dim != 64 && c->head_dim != 128) return false;
   if (c->page_size < 16 || c->page_size > 256 || c->page_size % 16 != 0) return false;
   if (c->code != HYB_CODE_E4M3 && c->code != HYB_CODE_INT8) return false;
+  // the tcgen05 form counts the rows of keys in 32 bits (64 bytes each at least: 256 GB)
+  if ((int64_t)c->n_pages * c->n_kv_heads >= 0xffffffffll / c->page_size) return false;
   if (b->batch < 1 || b->table_stride < 1 || (int64_t)b->table_stride * c->page_size > ((int64_t)1 << 30)) return false;
   if ((int64_t)b->batch * c->n_kv_heads > 65535) return false;
   // 32-token stages of all sequences and KV heads are counted in 31 bits
@@ -95,9 +97,7 @@ Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int
   int64_t len = std::min<int64_t>(b->max_len, (int64_t)b->table_stride * c->page_size);
   if (window > 0) len = std::min<int64_t>(len, (int64_t)window + sink + b->max_new + 64);
   const size_t row_bytes = (size_t)(c->head_dim + 4) * sizeof(float);
-  // the tcgen05 form places codes in 16-byte pieces of 32 bits (64 GB of keys, and of values)
-  const bool fits = (int64_t)c->n_pages * c->n_kv_heads * c->page_size * (c->head_dim / 16) < 0xffffffffll;
-  const bool mma = rows > kNarrowMost && type == HYB_TYPE_BF16 && fits;
+  const bool mma = rows > kNarrowMost && type == HYB_TYPE_BF16;
   p.form = mma ? Plan::kMma : rows <= kNarrowRows ? Plan::kNarrow : Plan::kWide;
   const int tile = mma ? kMmaRows : kWideRows;
   if (p.form == Plan::kNarrow || (mma && rows <= tile)) {

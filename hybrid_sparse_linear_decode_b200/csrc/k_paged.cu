@@ -420,7 +420,7 @@ __device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, floa
     *reinterpret_cast<float4*>(o + 2 * j) = make_float4(R.o[n][j][c] * f, R.o[n][j][2 + c] * f, R.o[n][j + 1][c] * f, R.o[n][j + 1][2 + c] * f);
 }
 
-// ---- the narrow form: up to 64 rows a KV head -----------------------------------------------------
+// ---- the narrow form: up to 32 bf16 rows a KV head, 64 of fp16 ------------------------------------
 //
 // Bound by the codes' bytes.  The stages of all (sequence, KV head) units form one
 // line that the CTAs cut into equal parts, so ragged batches keep every SM busy
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tiles_kernel(const Pa
   if (lane < D / 4) store_joined(p, seq.t0 + row / p.G, h * p.G + row % p.G, D, lane, y, m, l);
 }
 
-// ---- the wide form: many rows a KV head --------------------------------------------------------------
+// ---- the wide form: many fp16 rows a KV head ---------------------------------------------------------
 //
 // A CTA takes 64 rows, 16 a warp, and passes the stages its rows can see through
 // one shared ring; every warp converts the codes itself (the conversions run
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tiles_kernel(const Pa
 
 constexpr int kWideRing = 4;
 
-template <int D, bool INT8, bool FINE>
+template <int D, bool INT8>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(const PagedAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int NT = 2, kBytes = StageGeo<D>::kBytes, kRowFloats = D + 4;
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
     cp_commit();
     int sb, se;
     stage_range(span, i, sb, se);
-    if (sb <= R.pos_max) do_stage<D, INT8, NT, FINE>(p, smem + (i - s0) % kWideRing * kBytes, Q, R, sb);
+    if (sb <= R.pos_max) do_stage<D, INT8, NT, true>(p, smem + (i - s0) % kWideRing * kBytes, Q, R, sb);
   }
   cp_wait<0>();
   finish_sums<D, NT>(R);
@@ -917,20 +917,20 @@ cudaError_t narrow(const PagedAttnParams& p, cudaStream_t s) {
 }
 template <int D, bool INT8, bool FINE>
 cudaError_t narrow(const PagedAttnParams& p, int rows, cudaStream_t s) {
-  switch (rows) {
-    case 8: return narrow<D, INT8, 1, 1, FINE>(p, s);
-    case 16: return narrow<D, INT8, 2, 1, FINE>(p, s);
-    case 32: return narrow<D, INT8, 2, 2, FINE>(p, s);
-    default: return narrow<D, INT8, 2, 4, FINE>(p, s);
+  if (rows == 8) return narrow<D, INT8, 1, 1, FINE>(p, s);
+  if (rows == 16) return narrow<D, INT8, 2, 1, FINE>(p, s);
+  if constexpr (FINE) {
+    if (rows == 64) return narrow<D, INT8, 2, 4, FINE>(p, s);
   }
+  return narrow<D, INT8, 2, 2, FINE>(p, s);
 }
 
-template <int D, bool INT8, bool FINE>
+template <int D, bool INT8>
 cudaError_t wide(const PagedAttnParams& p, cudaStream_t s) {
   constexpr size_t smem = (size_t)kWideRing * StageGeo<D>::kBytes;
   static_assert(smem >= (size_t)kWarps * 8 * (D + 4) * sizeof(float), "the rows that leave fit");
   const int64_t tiles = ((int64_t)p.b.max_new * p.G + kWideRows - 1) / kWideRows;
-  cudaError_t e = launch(paged_wide_kernel<D, INT8, FINE>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
+  cudaError_t e = launch(paged_wide_kernel<D, INT8>, dim3((unsigned)(tiles * p.n_splits), p.b.B * p.c.Hkv),
                          dim3(kWarps * 32), smem, true, s, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   return launch(paged_join_rows_kernel<D>, dim3(p.Hq, p.b.max_new, p.b.B), dim3(kJoinThreads), 0, true, s, p);
@@ -959,12 +959,8 @@ cudaError_t launch_paged_narrow(const PagedAttnParams& p, int D, int int8, int r
 }
 
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int D, int int8, cudaStream_t s) {
-  if (p.half) {
-    if (D == 128) return int8 ? wide<128, true, true>(p, s) : wide<128, false, true>(p, s);
-    return int8 ? wide<64, true, true>(p, s) : wide<64, false, true>(p, s);
-  }
-  if (D == 128) return int8 ? wide<128, true, false>(p, s) : wide<128, false, false>(p, s);
-  return int8 ? wide<64, true, false>(p, s) : wide<64, false, false>(p, s);
+  if (D == 128) return int8 ? wide<128, true>(p, s) : wide<128, false>(p, s);
+  return int8 ? wide<64, true>(p, s) : wide<64, false>(p, s);
 }
 
 }  // namespace hyb

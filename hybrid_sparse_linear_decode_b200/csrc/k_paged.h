@@ -59,12 +59,12 @@ struct PagedAttnParams {
 };
 
 // Rows (new tokens x heads of a group) of one sequence and KV head that the
-// narrow form takes, and those of a CTA of the wide form.
+// narrow form takes in fp16, and those of a CTA of the wide form (fp16 only).
 constexpr int kNarrowRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kCtasPerSm = 3;
 constexpr int kPagedMaxCluster = 8;
-// Rows of a CTA of the form on tcgen05.
+// Rows of a CTA of the form on tcgen05 (bf16 only).
 constexpr int kMmaRows = 128;
 constexpr int kMmaCtasPerSm = 2;
 

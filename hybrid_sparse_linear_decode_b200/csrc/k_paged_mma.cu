@@ -1,4 +1,4 @@
-// Attention over the paged 8-bit cache for many query rows, on the tensor cores' own memory (tcgen05).
+// Attention over the paged 8-bit cache for many bf16 query rows, on the tensor cores' own memory (tcgen05).
 //
 // A CTA takes 128 rows and passes the tokens they can see 128 at a time:
 //   four converting warps turn the tile's codes into f16 in shared memory (the next tile's codes are on their way in
@@ -166,8 +166,8 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
     if (x.s0 >= x.s1) continue;
     const int32_t* table = p.b.table + (int64_t)x.b * p.b.mp;
     Pieces<D> c;
-    // where this thread's pieces of the tile to be loaded next begin, in pieces (kNone: no token there), and the page of
-    // this thread's group's scales
+    // the rows in which this thread's pieces of the tile to be loaded next lie (kNone: no token there), and the page of this
+    // thread's group's scales
     constexpr uint32_t kNone = 0xffffffffu;
     uint32_t from[kN];
     int entry[kN], gpage = -1, base, end;
@@ -185,14 +185,14 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
         const int tok = base + tid / kPerRow + i * kStep;
         const int in = tok - (p.c.P == 16 ? tok >> 4 : (int)__umulhi((uint32_t)tok >> 4, magic)) * p.c.P;
         from[i] = (uint32_t)entry[i] < (uint32_t)p.c.n_pages && tok < end
-                      ? (((uint32_t)entry[i] * p.c.Hkv + x.h) * p.c.P + in) * kPerRow + tid % kPerRow
+                      ? ((uint32_t)entry[i] * p.c.Hkv + x.h) * p.c.P + in
                       : kNone;
       }
     };
     auto load = [&](const uint8_t* codes, uint4 (&to)[kN]) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        to[i] = from[i] != kNone ? *(reinterpret_cast<const uint4*>(codes) + from[i]) : make_uint4(0, 0, 0, 0);
+        to[i] = from[i] != kNone ? *reinterpret_cast<const uint4*>(codes + (size_t)from[i] * D + tid % kPerRow * 16) : make_uint4(0, 0, 0, 0);
     };
     auto load_scales = [&]() {
       ks = vs = 0.f;
@@ -268,7 +268,6 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
   using Geo = MmaGeo<D>;
   const uint32_t sm = smem_u32(smem);
   const int warp = tid >> 5;
-  const bool half = p.half != 0;
   const uint32_t mine = tmem + ((uint32_t)(32 * warp) << 16);  // this warp's lanes
   Work w;
   Piece x;
@@ -290,15 +289,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
       {
         const uint16_t* src = p.q + tok * p.q_stride + (int64_t)hd * D;
         uint4 z[D / 8];
-        float amax = 0.f;
+        uint32_t most = 0;  // magnitudes of bf16 order as integers
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           z[i] = there ? *(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(in_lo(u[e], half)), fabsf(in_hi(u[e], half))));
+          for (int e = 0; e < 4; ++e) most = __vmaxu2(most, u[e] & 0x7fff7fffu);
         }
-        const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
+        const uint32_t e = min(max(max(most & 0xffffu, most >> 16) >> 7, 1u), 253u);
         const float inv = pow2_of(254u - e);
         rf = pow2_of(e) * p.scale;
 #pragma unroll
@@ -306,7 +305,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
           const uint32_t u[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
           uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = pack_half(in_lo(u[k], half) * inv, in_hi(u[k], half) * inv);
+          for (int k = 0; k < 4; ++k) y[k] = pack_half(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv);
           *reinterpret_cast<uint4*>(smem + Geo::kQ + (i / 8) * Geo::kSubTile + tid * 128 + (((i % 8) ^ (tid & 7)) * 16)) =
               make_uint4(y[0], y[1], y[2], y[3]);
         }
@@ -454,8 +453,8 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, uint8_t* 
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<uint2*>(to + i) =
-                make_uint2(pack_out(__uint_as_float(r[i]) * f, __uint_as_float(r[i + 1]) * f, half),
-                           pack_out(__uint_as_float(r[i + 2]) * f, __uint_as_float(r[i + 3]) * f, half));
+                make_uint2(pack_bf16(__uint_as_float(r[i]) * f, __uint_as_float(r[i + 1]) * f),
+                           pack_bf16(__uint_as_float(r[i + 2]) * f, __uint_as_float(r[i + 3]) * f));
         } else if (there) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)

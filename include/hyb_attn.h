@@ -435,8 +435,8 @@ const char* hyb_attn_strerror(int code);
 
 /* One layer's cache.  Codes [n_pages][n_kv_heads][page_size][head_dim], scales
  * fp32 [n_pages][n_kv_heads].  head_dim 64 or 128; page_size a multiple of 16,
- * at most 256; code pointers 16-byte aligned, scales 4-byte.  Pages never
- * written need no initial value. */
+ * at most 256; code pointers 16-byte aligned, scales 4-byte; n_pages * n_kv_heads *
+ * page_size below 2^32.  Pages never written need no initial value. */
 typedef struct hyb_attn_paged_cache {
   void*  k_codes;
   void*  v_codes;

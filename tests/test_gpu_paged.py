@@ -608,6 +608,32 @@ def test_attend_long_cache_and_far_pages():
     assert torch.equal(k[n - 5:], small.k_pages) and not k[:n - 5].any()
 
 
+def test_attend_pages_past_64_gigabytes():
+    """Codes past 2^32 pieces of 16 bytes, for every form (one buffer as keys and values; only its last pages are written)."""
+    import torch
+    import hybrid_sparse_linear_decode_b200 as H
+    page, Hkv, d = 128, 8, 128
+    n = (1 << 36) // (page * Hkv * d) + 4
+    free, _ = torch.cuda.mem_get_info()
+    if free < 80 << 30:
+        pytest.skip("needs 80 GB")
+    codes = torch.empty((n, Hkv, page, d), dtype=torch.int8, device="cuda")
+    g = torch.Generator("cuda").manual_seed(0)
+    codes[n - 4:] = torch.randint(-127, 128, (4, Hkv, page, d), generator=g, device="cuda", dtype=torch.int8)
+    s = torch.full((n, Hkv), 0.01, device="cuda")
+    far = H.PagedKVCache.from_tensors(codes, codes, s, s)
+    near = H.PagedKVCache.from_tensors(codes[n - 4:].clone(), codes[n - 4:].clone(), s[:4].clone(), s[:4].clone())
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    at = ints([[2, 0, 3, 1]])
+    for new in (1, 8, 12, 60):
+        for dtype in (torch.bfloat16, torch.float16):
+            q = torch.randn(new, 32, d, generator=g, device="cuda").to(dtype)
+            outs = [c.attend(q, ints([0, new]), ints([500]), t, max_new=new, max_len=500) for c, t in ((far, at + (n - 4)), (near, at))]
+            assert torch.equal(*outs) and far.status() == near.status() == 0
+    del far, codes
+    torch.cuda.empty_cache()
+
+
 # ---- streams, graphs, refusals -----------------------------------------------------------------------
 def test_calls_on_another_stream():
     import torch

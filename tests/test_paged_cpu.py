@@ -105,7 +105,7 @@ def _batch(A, **kw):
     return A.hyb_attn_paged_batch(**b)
 
 
-BAD_CACHE = [dict(head_dim=96), dict(page_size=8), dict(page_size=24), dict(page_size=272), dict(n_pages=0), dict(n_kv_heads=0),
+BAD_CACHE = [dict(n_pages=1 << 26, n_kv_heads=4), dict(n_pages=(1 << 31) - 1, page_size=256), dict(head_dim=96), dict(page_size=8), dict(page_size=24), dict(page_size=272), dict(n_pages=0), dict(n_kv_heads=0),
              dict(code=2)]
 BAD_BATCH = [dict(batch=0), dict(table_stride=0), dict(table_stride=1 << 27), dict(n_new=-1), dict(max_new=3), dict(max_new=0),
              dict(max_len=-1), dict(batch=40000), dict(batch=30000, table_stride=1 << 18)]
@@ -243,3 +243,25 @@ def test_calls_refuse_tensors_of_the_host(A):
         binding().paged_attend(at, 0, 0, row, ints, ints[:2], ints[:2].view(2, 1), 1, 8, 0, 0, 0.0, None, False)
     with pytest.raises(ValueError, match="q has to be"):
         binding().delta_run(st, 0, 0, row, row, row, row, row, ints, 1, None, 0.0, None)
+
+
+@pytest.mark.parametrize("type", [0, 1])
+@pytest.mark.parametrize("head_dim,G", [(64, 1), (64, 16), (128, 4), (128, 8)])
+def test_workspace_of_any_window_and_type_fits_the_workspace_asked_for(A, type, head_dim, G):
+    """As above for both types, over more sequences, rows and lengths."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    rng = np.random.default_rng(head_dim + G)
+    some = 0
+    for _ in range(300):
+        B, new, pages = (int(np.exp(rng.uniform(0, np.log(x)))) for x in (200, 3000, 3000))
+        c = _cache(A, head_dim=head_dim)
+        b = _batch(A, batch=B, n_new=B * new, max_new=new, table_stride=pages, max_len=16 * pages)
+        size = A.hyb_attn_paged_workspace_size(c, b, 2 * G)
+        some += size > 0
+        for window in (0, 1, int(rng.integers(1, 16 * pages + 1)), int(rng.integers(1, 16 * pages + 1)), (1 << 31) - 1):
+            with pytest.raises(A.HybAttnError) as e:
+                A.hyb_attn_paged_attend(c, b, type, 256, 2 * G * head_dim, 512, 2 * G * head_dim, None, 2 * G, window, int(rng.integers(0, 100)), 0.0, 1024, size, None)
+            assert e.value.code == A.HYB_ECUDA, (B, new, pages, window)
+    assert some > 50

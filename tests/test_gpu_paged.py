@@ -564,6 +564,49 @@ def test_attend_many_sequences():
     c.check_attend([1 if n else 0 for n in lens], 4)
 
 
+def needs_workspace(c, new, Hq, window=0, n_sink=0):
+    """Whether the call's parts go through the workspace (a line of all units' stages that CTAs share, or split row tiles):
+    without one it is refused before anything is launched."""
+    import hybrid_sparse_linear_decode_b200 as H
+    q = c.rows(sum(new), Hq)
+    keep = [c.ints(np.concatenate([[0], np.cumsum(new)])), c.ints(c.lens), c.ints(c.table), q]
+    b = H.hyb_attn_paged_batch(keep[2].data_ptr(), keep[0].data_ptr(), keep[1].data_ptr(), len(new), c.table.shape[1], sum(new), max(new), max(c.lens), 0)
+    try:
+        H.hyb_attn_paged_attend(c.h._c, b, {"bf16": H.HYB_TYPE_BF16, "fp16": H.HYB_TYPE_FP16}[c.dtype], q.data_ptr(), Hq * c.d,
+                                c.torch.empty_like(q).data_ptr(), Hq * c.d, None, Hq, window, n_sink, 0.0, None, 0,
+                                c.torch.cuda.current_stream().cuda_stream)
+    except H.HybAttnError as e:
+        return e.code == -6
+    return False
+
+
+RAGGED = np.random.default_rng(33).integers(0, 5000, 45).tolist()
+RAGGED[3], RAGGED[40], RAGGED[44] = 0, 4999, 5000
+
+
+@pytest.mark.parametrize("kind,dtype,d", [("e4m3", "bf16", 128), ("int8", "fp16", 128), ("int8", "bf16", 64), ("e4m3", "fp16", 64)])
+@pytest.mark.parametrize("lens,new,Hkv,G,page,window,n_sink", [
+    ([4096], [1], 2, 4, 64, 0, 0),                       # one sequence
+    ([4097, 9000], [1, 1], 1, 8, 16, 0, 0),
+    ([5001, 0, 4100], [3, 0, 8], 2, 4, 48, 0, 0),        # drafts, and an empty sequence between
+    ([5000, 7, 6100], [2, 2, 1], 1, 5, 64, 0, 0),        # a short one between long ones
+    ([6000, 4999], [8, 5], 1, 2, 128, 2500, 5),          # a window that begins inside a page
+    ([4500, 33], [1, 1], 1, 4, 32, 4000, 0),
+    ([5000, 4096], [8, 7], 1, 8, 64, 0, 0),              # 64 rows: fp16 on the line, bf16 on tcgen05's
+    ([7000, 4100], [16, 3], 1, 8, 32, 3000, 40),         # 128 rows
+    (RAGGED, [1 if n else 0 for n in RAGGED], 1, 4, 64, 0, 0),         # more sequences than a warp has lanes
+    (RAGGED, [min(3, n) for n in RAGGED], 1, 4, 16, 1700, 3),
+    (RAGGED, [min(9 + i % 3, n) for i, n in enumerate(RAGGED)], 1, 4, 64, 0, 0)])
+def test_attend_line(kind, dtype, d, lens, new, Hkv, G, page, window, n_sink):
+    """Long sequences, whose units' stages lie on one line that the CTAs cut into equal parts, and their joins."""
+    c = Paged(lens, page, Hkv, d, kind, dtype, seed=d + len(lens))
+    rows = max(new) * G
+    if dtype == "bf16" or rows <= 64:      # beyond, fp16 goes in row tiles
+        assert needs_workspace(c, new, Hkv * G, window, n_sink)
+    c.check_attend(new, Hkv * G, window, n_sink, tail=1)
+    assert c.h.status() == 0
+
+
 @pytest.mark.parametrize("lens,new,Hkv,G,window", [
     ([2300], [330], 8, 8, 0),               # 168 row tiles: fewer than the SMs hold, in parts
     ([2100, 90], [640, 90], 4, 8, 0),       # 320, many of them without rows; the last ones in parts
@@ -678,6 +721,36 @@ def test_two_captured_graphs_share_a_cache():
         torch.cuda.synchronize()
         for g, q, out in graphs:
             assert torch.equal(out, c.h.attend(q, cu, lens, table, 1, 200))
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_two_captured_graphs_on_the_line(new):
+    """As above with sequences whose parts go through workspaces, replayed at once on two streams with other lengths."""
+    import torch
+    c = Paged([5000, 4200], 64, 1, 128, seed=29)
+    assert needs_workspace(c, [new, new], 4)
+    table, lens, cu = c.ints(c.table), c.ints([5000, 4200]), c.ints([0, new, 2 * new])
+    graphs = []
+    for i in range(2):
+        q = c.rows(2 * new, 4)
+        c.h.attend(q, cu, lens, table, new, 5000)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = c.h.attend(q, cu, lens, table, new, 5000)
+        graphs.append((g, q, out))
+    for n0, n1 in ((5000, 4200), (3000, 64), (64, 4199)):
+        lens.copy_(c.ints([n0, n1]))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for _ in range(20):
+            for (g, q, out), s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for g, q, out in graphs:
+            assert torch.equal(out, c.h.attend(q, cu, lens, table, new, 5000))
+    assert c.h.status() == 0
 
 
 def test_calls_refuse_what_they_do_not_take():

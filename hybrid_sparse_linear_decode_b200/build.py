@@ -2,7 +2,8 @@
 
 Objects are compiled in parallel under ``_build/`` and linked with the static
 CUDA runtime, so the library carries its own runtime and needs no JIT cache.
-``_binding.so`` (the calls that take PyTorch tensors) is linked against it.
+``_binding.so`` (the calls that take PyTorch tensors) is linked against it; it alone needs
+PyTorch and Python's headers, and the library is there whether it can be built or not.
 """
 
 from __future__ import annotations
@@ -82,7 +83,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
         binding = ex.submit(compile_binding, force)
         logs = list(ex.map(compile_one, srcs, objs))
-        binding = binding.result()
     if verbose:
         for lg in logs:
             if lg:
@@ -93,6 +93,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    try:
+        binding = binding.result()
+    except Exception as e:
+        raise RuntimeError(f"{LIB} is built; {os.path.basename(BINDING)} (PagedKVCache, GatedDeltaState) is not: {e}") from e
     if force or _stale(BINDING, [binding]):
         link_binding(binding)
     return LIB

@@ -265,3 +265,21 @@ def test_workspace_of_any_window_and_type_fits_the_workspace_asked_for(A, type, 
                 A.hyb_attn_paged_attend(c, b, type, 256, 2 * G * head_dim, 512, 2 * G * head_dim, None, 2 * G, window, int(rng.integers(0, 100)), 0.0, 1024, size, None)
             assert e.value.code == A.HYB_ECUDA, (B, new, pages, window)
     assert some > 50
+
+
+# ---- the build -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("what", [ImportError("no PyTorch"), RuntimeError("Python.h: no such file")])
+def test_the_library_is_linked_without_the_binding(monkeypatch, tmp_path, what):
+    """Without PyTorch or Python's headers only the calls that take tensors are missing."""
+    from hybrid_sparse_linear_decode_b200 import build as B
+    for name in ("LIB", "BINDING", "BUILD_DIR"):
+        monkeypatch.setattr(B, name, str(tmp_path / name))
+    monkeypatch.setattr(B, "SOURCES", ["api_delta.cu"])
+
+    def fails(force):
+        raise what
+
+    monkeypatch.setattr(B, "compile_binding", fails)
+    with pytest.raises(RuntimeError, match="is built"):
+        B.build()
+    assert (tmp_path / "LIB").exists() and not (tmp_path / "BINDING").exists()

@@ -23,6 +23,16 @@ def binding():
     return _binding
 
 
+def read_status(word: torch.Tensor, clear: bool) -> int:
+    """A handle's status word once all work on its device is done: its calls may have been made, or replayed, on any stream."""
+    torch.cuda.synchronize(word.device)
+    flags = int(word.item())
+    if clear:
+        word.zero_()
+        torch.cuda.synchronize(word.device)  # before whatever another stream raises next
+    return flags
+
+
 def on_stream(stream, device: torch.device):
     """The caller's stream as the current one, so that what a call allocates belongs to the stream that uses it."""
     if not isinstance(stream, torch.cuda.Stream):

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _abi as A
-from ._tensors import binding, need, on_stream
+from ._tensors import binding, need, on_stream, read_status
 
 
 class GatedDeltaState:
@@ -60,8 +60,5 @@ class GatedDeltaState:
         return self._calls.delta_run(self._c_at, self._index, self._status_at, q, k, v, g, beta, cu, max_new, slots, scale, out)
 
     def status(self, clear: bool = False) -> int:
-        """The HYB_STATUS_* bits raised by these states' calls so far (waits for them)."""
-        flags = int(self._status.item())
-        if clear:
-            self._status.zero_()
-        return flags
+        """The HYB_STATUS_* bits raised by these states' calls so far, on whatever stream (waits for the device)."""
+        return read_status(self._status, clear)

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _abi as A
-from ._tensors import binding, need, on_stream
+from ._tensors import binding, need, on_stream, read_status
 
 _CODES = {torch.float8_e4m3fn: A.HYB_CODE_E4M3, torch.int8: A.HYB_CODE_INT8}
 
@@ -89,8 +89,5 @@ class PagedKVCache:
                                         window, n_sink, scale, out, return_lse)
 
     def status(self, clear: bool = False) -> int:
-        """The HYB_STATUS_* bits raised by this cache's calls so far (waits for them)."""
-        flags = int(self._status.item())
-        if clear:
-            self._status.zero_()
-        return flags
+        """The HYB_STATUS_* bits raised by this cache's calls so far, on whatever stream (waits for the device)."""
+        return read_status(self._status, clear)

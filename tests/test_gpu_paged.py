@@ -753,6 +753,29 @@ def test_two_captured_graphs_on_the_line(new):
     assert c.h.status() == 0
 
 
+def test_status_waits_for_calls_on_other_streams():
+    """What a call raises on a busy stream of the caller's is there when the status is read from another one."""
+    import torch
+    import hybrid_sparse_linear_decode_b200 as H
+    c = Paged([64], 16, 2, 64, seed=30)
+    d = H.GatedDeltaState(1, 1, 1, 64, 64)
+    cu, bad, table, q, k = c.ints([0, 1]), c.ints([65]), c.ints(c.table[:, :4]), c.rows(1, 2), c.rows(1, 2)
+    row, gate, slot = c.rows(1, 1), torch.zeros(1, 1, device="cuda"), c.ints([5])
+    s = torch.cuda.Stream()
+    calls = [(c.h, H.HYB_STATUS_BAD_LENGTH, lambda: c.h.append(k, k, cu, bad, table, max_new=1, stream=s)),
+             (c.h, H.HYB_STATUS_BAD_LENGTH, lambda: c.h.attend(q, cu, bad, table, 1, 64, stream=s)),
+             (d, H.HYB_STATUS_BAD_SLOT, lambda: d.run(row, row, row, gate, gate, cu, max_new=1, slots=slot, stream=s))]
+    for h, flag, call in calls:
+        call()      # loads the kernel, which waits
+        torch.cuda.synchronize()
+        h.status(clear=True)
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+        call()
+        assert h.status(clear=True) == flag
+        assert h.status() == 0
+
+
 def test_calls_refuse_what_they_do_not_take():
     c = Paged([40], 16, 2, 64, seed=15)
     t, cu, lens, table = c.torch, c.ints([0, 1]), c.ints([40]), c.ints(c.table)

@@ -130,6 +130,14 @@ __device__ __forceinline__ void issue_stage(const PagedAttnParams& p, uint8_t* s
   }
 }
 
+// Zeros in place of the values that no row sees at the begin of a window: their weights are 0, but their codes may be NaN.
+// N threads, this one number `me`; the stage is there for all of them, and they meet afterwards.
+template <int D, int N>
+__device__ __forceinline__ void clear_gap(uint8_t* stage, int base, const Gap& gap, int me) {
+  for (int i = me; i < (gap.from - gap.gap) * (D / 16); i += N)
+    reinterpret_cast<uint4*>(stage + kStageTokens * D)[(gap.gap - base) * (D / 16) + i] = make_uint4(0, 0, 0, 0);
+}
+
 // A warp's rows: NT tiles of 8; this lane's are columns 2 t and 2 t + 1 of each (t = lane % 4).
 template <int D, int NT>
 struct Rows {
@@ -554,6 +562,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
       cp_commit();
       int sb, se;
       stage_range(span, s0 + team + i * kTeams, sb, se);
+      if (!INT8 && p.W > 0 && sb == span.lo) {
+        clear_gap<D, GW * 32>(ring + slot_out * kBytes, sb, gap_of(p, sb, pos0), me);
+        team_sync<GW>();
+      }
       if (sb <= R.pos_max) do_stage<D, INT8, NT, FINE>(p, ring + slot_out * kBytes, Q, R, sb);
       slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
       slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
@@ -851,6 +863,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_wide_kernel(con
     cp_commit();
     int sb, se;
     stage_range(span, i, sb, se);
+    if (!INT8 && p.W > 0 && sb == span.lo) {
+      clear_gap<D, kWarps * 32>(smem + (i - s0) % kWideRing * kBytes, sb, gap_of(p, sb, pos_min), threadIdx.x);
+      __syncthreads();
+    }
     if (sb <= R.pos_max) do_stage<D, INT8, NT, true>(p, smem + (i - s0) % kWideRing * kBytes, Q, R, sb);
   }
   cp_wait<0>();

@@ -110,6 +110,14 @@ __device__ __forceinline__ Span<T> make_span(int pos_min, int pos_max, int cap, 
   s.stages = s.sink_stages + (max(s.hi - s.lo, 0) + T - 1) / T;
   return s;
 }
+// The first stage of a window begins at a multiple of 16: no row sees its tokens [gap, from).
+struct Gap {
+  int gap, from;
+};
+__device__ __forceinline__ Gap gap_of(const PagedAttnParams& p, int lo, int pos_min) {
+  const int from = max(max(pos_min, 0) - p.W + 1, 0);
+  return Gap{min(max(lo, p.S), from), from};
+}
 template <int T>
 __device__ __forceinline__ void stage_range(const Span<T>& s, int st, int& base, int& end) {
   if (st < s.sink_stages) {

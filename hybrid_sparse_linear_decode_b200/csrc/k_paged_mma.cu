@@ -188,6 +188,14 @@ __device__ __forceinline__ void convert_role(const PagedAttnParams& p, uint8_t* 
                       ? ((uint32_t)entry[i] * p.c.Hkv + x.h) * p.c.P + in
                       : kNone;
       }
+      if (!INT8 && p.W > 0 && base == x.span.lo) {  // what no row sees at the window's begin: its codes may be NaN
+        const Gap gap = gap_of(p, base, x.seq.pos0 + x.row0 / p.G);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int tok = base + tid / kPerRow + i * kStep;
+          if (tok >= gap.gap && tok < gap.from) from[i] = kNone;
+        }
+      }
     };
     auto load = [&](const uint8_t* codes, uint4 (&to)[kN]) {
 #pragma unroll

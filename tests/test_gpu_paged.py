@@ -525,6 +525,33 @@ def test_attend_scales_of_pages_a_row_does_not_see(kind, dtype, G, new, step, ti
         check_positions(c, q[rows], out[rows], lse[rows], {j: first + i for j, i in enumerate(rows)}, 16 * -(-length // 16), window, 0, step)
 
 
+@pytest.mark.parametrize("dtype,G,new,step", [("bf16", 1, 1, 2.0 ** -39), ("bf16", 4, 4, 2.0 ** -39), ("bf16", 4, 20, 2.0 ** -31),
+                                              ("fp16", 2, 3, 2.0 ** -39), ("fp16", 16, 20, 2.0 ** -39)])
+@pytest.mark.parametrize("length,window,n_sink", [(200, 70, 0), (200, 70, 5), (200, 33, "between"), (200, 33, 16), (90, 1, 3), (5000, 4090, 7)])
+def test_attend_nothing_outside_the_window_is_used(dtype, G, new, step, length, window, n_sink):
+    """NaN codes wherever no row looks (in pages that hold visible tokens too), NaN scales of pages that hold none."""
+    c = Paged([length], 64, 1, 128, "e4m3", dtype, seed=31)
+    first = length - new
+    if n_sink == "between":     # sinks that end inside the 16 tokens in which the window begins
+        n_sink = ((first - window + 1) & ~15) + 2
+    unseen = [j for j in range(length) if j <= first - window and j >= n_sink]
+    assert unseen
+    for j in unseen:
+        for x in "kv":
+            c.codes[x][c.table[0, j // 64], :, j % 64] = 0x7f
+    for i in range(-(-length // 64)):
+        if all(j in set(unseen) for j in range(64 * i, min(64 * i + 64, length))):
+            for x in "kv":
+                c.scales[x][c.table[0, i]] = np.nan
+    for x in "kv":
+        c.t[x].view(c.torch.uint8).copy_(c.torch.from_numpy(c.codes[x]))
+        c.ts[x].copy_(c.torch.from_numpy(c.scales[x]))
+    q = c.rows(new, G)
+    out, lse = c.h.attend(q, c.ints([0, new]), c.ints([length]), c.ints(c.table), new, length, window=window, n_sink=n_sink, return_lse=True)
+    check_positions(c, q, out, lse, {i: first + i for i in range(new)}, 64 * -(-length // 64), window, n_sink, step)
+    assert c.h.status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_attend_large_and_tiny_values(dtype):
     """Queries of very different sizes, scales of pages 2^40 apart, logits far apart."""

@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_narrow_kernel(c
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i) {
-          const float w = m == -INFINITY ? 0.f : exp2_fast(e[i].x - m) * e[i].y;
+          const float w = part_weight(e[i].x, e[i].y, m);
           l += w;
           y.x += w * o[i].x, y.y += w * o[i].y, y.z += w * o[i].z, y.w += w * o[i].w;
         }
@@ -680,7 +680,7 @@ __device__ __forceinline__ float4 join_parts(int n, F part, float& top, float& s
 #pragma unroll
   for (int k = 0; k < kJoinMost / kJoinThreads; ++k) {
     const int i = tid + k * kJoinThreads;
-    const float w = m == -INFINITY ? 0.f : exp2_fast(e[k].x - m) * e[k].y;
+    const float w = part_weight(e[k].x, e[k].y, m);
     if (i < n) weight[i] = w;
     l += w;
   }
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tiles_kernel(const Pa
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float w[2], l;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) w[k] = m == -INFINITY ? 0.f : exp2_fast(e[k].x - m) * e[k].y;
+  for (int k = 0; k < 2; ++k) w[k] = part_weight(e[k].x, e[k].y, m);
   l = w[0] + w[1];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

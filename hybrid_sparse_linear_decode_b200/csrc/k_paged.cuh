@@ -221,7 +221,10 @@ __device__ __forceinline__ void store_row(const PagedAttnParams& p, int64_t tok,
 
 constexpr float kLn2 = 0.6931471805599453f;
 // Natural logarithm of the sum whose weights are 2^(z - m + 15).
-__device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m - 15.f + log2f(l)) * kLn2; }
+// A row without a maximum saw nothing (l = 0), or NaN logits only (l is NaN).
+__device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? (l == 0.f ? -INFINITY : l) : (m - 15.f + log2f(l)) * kLn2; }
+// What a part with maximum pm and sum pl weighs beside the largest maximum m.
+__device__ __forceinline__ float part_weight(float pm, float pl, float m) { return m == -INFINITY ? pl : exp2_fast(pm - m) * pl; }
 
 __device__ __forceinline__ void store_joined(const PagedAttnParams& p, int64_t tok, int hd, int D, int c, const float4& y,
                                              float m, float l) {

@@ -578,6 +578,19 @@ def test_attend_non_finite_queries_stay_in_their_rows():
         assert bad[1, 0] and bad[2, 1] and bad.sum() == 2
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("length,new,G", [(70, 3, 2), (70, 50, 2), (5000, 3, 2), (5000, 12, 4), (5000, 150, 2)])
+def test_attend_sums_of_rows_that_are_not_finite(dtype, length, new, G):
+    """A NaN output has a NaN logarithm of its sum: -inf would pass for a row that sees nothing where rows are merged."""
+    c = Paged([length], 64, 1, 64, dtype=dtype, seed=32)
+    q = c.rows(new, G)
+    q[1, 0, 3], q[2, 1, 5] = float("nan"), float("inf")
+    out, lse = c.h.attend(q, c.ints([0, new]), c.ints([length]), c.ints(c.table), new, length, return_lse=True)
+    bad = np.isnan(f64(out)).any(-1)
+    assert bad[1, 0] and bad[2, 1] and bad.sum() == 2
+    assert np.array_equal(np.isnan(f64(lse)), bad)
+
+
 def test_attend_strided_rows_and_scale():
     c = Paged([50, 120], 32, 2, 128, "e4m3", "fp16", seed=11)
     c.check_attend([2, 3], 6, wide=5, scale=0.3)

@@ -61,6 +61,12 @@ int32_t int_of(int64_t x, const char* name) {
   return (int32_t)x;
 }
 
+// 0 selects a default, so what 32 bits would turn into 0 is refused.
+float scale_of(double x) {
+  if (x != 0 && (float)x == 0.f) refuse("scale does not fit 32 bits");
+  return (float)x;
+}
+
 hyb_attn_paged_batch batch_of(int64_t index, int64_t status, const Tensor& cu, const Tensor& lens, const Tensor& table,
                               int64_t rows, int64_t max_new, int64_t max_len) {
   if (table.dim() != 2) refuse("page_table has to be [B, pages], not " + text_of(table));
@@ -127,6 +133,7 @@ py::object paged_attend(int64_t cache_at, int64_t index, int64_t status, const T
                         const Tensor& table, int64_t max_new, int64_t max_len, int64_t window, int64_t n_sink, double scale,
                         const OptTensor& out, bool return_lse) {
   const auto& c = *reinterpret_cast<const hyb_attn_paged_cache*>(cache_at);
+  const float factor = scale_of(scale);
   const int type = type_of(q, "q");
   if (q.dim() != 3) refuse("q has to be [rows, n_q_heads, head_dim], not " + text_of(q));
   const int64_t n = q.size(0), heads = q.size(1);
@@ -148,7 +155,7 @@ py::object paged_attend(int64_t cache_at, int64_t index, int64_t status, const T
   if (size > 0) ws = at::empty({(int64_t)size}, q.options().dtype(at::kByte));
   const int rc = hyb_attn_paged_attend(&c, &b, type, q.const_data_ptr(), qs, to.data_ptr(), os,
                                        return_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, (int32_t)heads,
-                                       int_of(window, "window"), int_of(n_sink, "n_sink"), (float)scale,
+                                       int_of(window, "window"), int_of(n_sink, "n_sink"), factor,
                                        size > 0 ? ws.data_ptr() : nullptr, size,
                                        c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream());
   if (rc < 0) fail("hyb_attn_paged_attend", rc);
@@ -159,6 +166,7 @@ py::object paged_attend(int64_t cache_at, int64_t index, int64_t status, const T
 Tensor delta_run(int64_t state_at, int64_t index, int64_t status, const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& g,
                  const Tensor& beta, const Tensor& cu, int64_t max_new, const OptTensor& slots, double scale, const OptTensor& out) {
   const auto& s = *reinterpret_cast<const hyb_attn_delta_state*>(state_at);
+  const float factor = scale_of(scale);
   const int64_t qs = rows_of(q, "q", s.n_k_heads, s.key_dim, index, at::kBFloat16);
   const int64_t ks = rows_of(k, "k", s.n_k_heads, s.key_dim, index, at::kBFloat16);
   const int64_t vs = rows_of(v, "v", s.n_v_heads, s.value_dim, index, at::kBFloat16);
@@ -182,7 +190,7 @@ Tensor delta_run(int64_t state_at, int64_t index, int64_t status, const Tensor& 
     to = at::empty({n, s.n_v_heads, s.value_dim}, q.options());
   }
   const int rc = hyb_attn_delta_run(&s, q.const_data_ptr(), qs, k.const_data_ptr(), ks, v.const_data_ptr(), vs, gp, bp, to.data_ptr(), os,
-                                    cup, sp, int_of(B, "B"), int_of(n, "rows"), (int32_t)std::min(max_new, n), (float)scale,
+                                    cup, sp, int_of(B, "B"), int_of(n, "rows"), (int32_t)std::min(max_new, n), factor,
                                     reinterpret_cast<uint32_t*>(status),
                                     c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream());
   if (rc < 0) fail("hyb_attn_delta_run", rc);

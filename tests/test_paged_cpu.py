@@ -267,6 +267,19 @@ def test_workspace_of_any_window_and_type_fits_the_workspace_asked_for(A, type, 
     assert some > 50
 
 
+@pytest.mark.parametrize("scale", [1e-50, -1e-50, 5e-324])
+def test_calls_refuse_a_scale_that_would_select_the_default(A, scale):
+    """0 selects 1/sqrt(d); a scale that is 0 only in 32 bits is not one of them."""
+    import torch
+    from hybrid_sparse_linear_decode_b200._tensors import binding
+    c, s = _cache(A), A.hyb_attn_delta_state(256, 4, 2, 4, 64, 128)
+    row, ints = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scale"):
+        binding().paged_attend(ctypes.addressof(c), 0, 0, row, ints, ints[:2], ints[:2].view(2, 1), 1, 8, 0, 0, scale, None, False)
+    with pytest.raises(ValueError, match="scale"):
+        binding().delta_run(ctypes.addressof(s), 0, 0, row, row, row, row, row, ints, 1, None, scale, None)
+
+
 # ---- the build -----------------------------------------------------------------------------------------
 @pytest.mark.parametrize("what", [ImportError("no PyTorch"), RuntimeError("Python.h: no such file")])
 def test_the_library_is_linked_without_the_binding(monkeypatch, tmp_path, what):

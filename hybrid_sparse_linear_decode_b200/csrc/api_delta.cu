@@ -12,8 +12,10 @@ using namespace hyb;
 namespace {
 
 // From this many tokens a sequence the chunks are faster than single steps: 4 sequences of 32 heads of 128 x 128, steps /
-// chunks: 8 tokens 9.4 / 13.1 us, 12 12.5 / 13.1, 16 15.4 / 13.1, 64 51.7 / 13.5; 32 sequences: 8 tokens 62.5 / 91.2, 12 84.8 /
-// 91.6, 16 106.7 / 91.7, 64 375 / 97.
+// chunks: 8 tokens 9.1 / 12.9 us, 12 12.1 / 13.0, 16 15.1 / 13.0, 64 51.7 / 13.5; 32 sequences: 8 tokens 62.3 / 91.4, 12 84.1 /
+// 91.5, 16 106.5 / 91.8, 64 375 / 97; 4 heads, 4 sequences: 12 tokens 11.9 / 12.5, 16 14.9 / 12.5; heads of 64 x 64, 4 sequences:
+// 12 8.8 / 10.3, 16 11.1 / 10.3.  Not so where heads of 64 x 64 are more than the SMs, whose steps share an SM and whose chunks
+// do not: 32 sequences of 32, 16 tokens 25.4 / 66.4, 24 36.0 / 66.8.
 constexpr int kChunksFrom = 14;
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

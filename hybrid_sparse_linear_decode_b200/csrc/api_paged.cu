@@ -70,23 +70,28 @@ struct Plan {
 
 // Up to kNarrowMost rows a KV head: narrow, 8 or 16 rows a warp, bound by the codes' bytes.  More: bf16 on tcgen05, in
 // whose 128 rows one conversion of the codes serves all; fp16, whose weights go in as two parts, on the warps' own
-// products (narrow up to 64 rows, then wide).  8 sequences of up to 32K tokens, 4 rows a token, narrow / tcgen05: 20
-// rows 162 / 178 us, 32 rows 169 / 179, 48 rows 294 / 208, 64 rows 303 / 204.
+// products (narrow up to 64 rows, then wide).  8 sequences of up to 32K tokens, 8 KV heads of 128, 4 rows a token, narrow /
+// tcgen05: 20 rows 151 / 161 us, 32 rows 158 / 163; heads of 64, int8: 102 / 136, 105 / 138; 2 KV heads: 52 / 53, 57 / 53;
+// one sequence of 4096: 14.9 / 14.1, 15.8 / 16.1.  48 rows took 294 / 208 and 64 rows 303 / 204 when measured; tcgen05 takes
+// 199 and 194 now.
 // While a sequence's rows fit one tile the CTAs share the line of all tiles; more rows, and few row tiles, cut each row
 // tile's tokens into as many parts as the SMs hold at once, each of at least kLeastTokens (128 tokens of one sequence,
 // parts of at least 128 / 256 / 512 / 1024 tokens: of 1024 tokens 26 / 23 / 28 / 34 us, of 2048 41 / 30 / 29 / 40).
 constexpr int kNarrowMost = 32;
 constexpr int kLeastTokens = 256;
 // On tcgen05, row tiles that fill the SMs more than half, or come behind full turns of them, go in parts of at least
-// kLeastTail tokens (512 / 1024 / 2048 / whole: 2047 tokens of 10001 608 / 608 / 608 / 639 us, 1300 of 8192 335 / 334 / 325 /
-// 440, 1300 of 4096 171 / 172 / 189 / 211, 700 of 4096 141 / 129 / 144 / 144, 2048 of 2048 136 / 98 / 98 / 98).
+// kLeastTail tokens (512 / 1024 / 2048 / whole, when a tile took 5 % more than it does: 2047 tokens of 10001 608 / 608 / 608 /
+// 639 us, 1300 of 8192 335 / 334 / 325 / 440, 1300 of 4096 171 / 172 / 189 / 211, 700 of 4096 141 / 129 / 144 / 144, 2048 of
+// 2048 136 / 98 / 98 / 98).
 constexpr int kLeastTail = 1024;
 // The narrow form by clusters or by the line: a cluster's CTA takes stages / CTAs stages of 32 tokens; on the line it
 // takes an equal share of all, and the second launch that joins the parts costs about kLineStages stages' time.  (What a
 // length gives to clusters, every shorter one does too, so a window needs no workspace that no window does not.)  One
-// token each, 4096 tokens, 8 KV heads, clusters / line: 8 sequences 18.9 / 21.0 us, 16 28.7 / 32.1; 32 sequences of 2048
-// 34.7 / 32.9, of 1024 20.4 / 22.0; 8 of 16384 49.2 / 52.2, of 32768 94.1 / 93.4.  Clusters above 8 are not used: 4
-// sequences of 4096 in clusters of 13 20.2 / 15.5, 2 in clusters of 16 11.6 / 11.9, 1 of 16384 17.7 / 16.4.
+// token each, 4096 tokens, 8 KV heads of 128, clusters / line: 8 sequences 18.6 / 21.4 us, 16 28.8 / 31.8; 32 sequences of
+// 2048 34.9 / 32.4, of 1024 20.4 / 22.0; 64 of 1024 35.1 / 36.1; 8 of 16384 49.2 / 52.2, of 32768 94.1 / 93.4.  Heads of 64,
+// int8, fp16: 8 of 4096 15.1 / 17.0, 32 of 2048 28.5 / 27.4, 64 of 1024 27.2 / 30.8; 2 KV heads of 8 query heads each: 16 of
+// 4096 16.4 / 16.3, 32 of 2048 13.3 / 16.5; one KV head: 64 of 1024 9.7 / 12.1.  Clusters above 8 are not used: 4 sequences
+// of 4096 in clusters of 13 20.2 / 15.5, 2 in clusters of 16 11.6 / 11.9, 1 of 16384 17.7 / 16.4.
 constexpr int64_t kLineStages = 8;
 
 Plan make_plan(const hyb_attn_paged_cache* c, const hyb_attn_paged_batch* b, int Hq, int window, int sink, int type) {

@@ -43,7 +43,8 @@ __device__ __forceinline__ Run read_run(const DeltaParams& p, int b, bool tell) 
 // rows in a run, so its keys are a contiguous piece of k), reads and writes it once, and takes the tokens
 // through it.  S^T k and S^T q of the old state come from one pass over the registers:
 // u = beta (v - a S^T k), o = scale (a S^T q + (k . q) u), and the second pass forms a S + k u^T.
-// 64 sequences of 32 heads of 128 x 128, one token: 45 us, 6.0 TB/s; one sequence: 3.7 us, latency.
+// 64 sequences of 32 heads of 128 x 128, one token: 45 us, 6.0 TB/s; one sequence: 4.6 us, latency.  More tokens take
+// 0.75 us each for one sequence, 5.5 for 32: the next token's rows are asked for behind the last use of the present ones.
 
 template <int DK>
 struct Piece {

@@ -437,10 +437,10 @@ __device__ __forceinline__ void put_row(const Rows<D, NT>& R, int n, int c, floa
 // more than one CTA worked on is joined by paged_join_kernel.  Short sequences are bound by
 // latency instead: a cluster of CTAs takes each unit and joins it itself, in one launch.
 //
-// 8 KV heads of 128, 4 query heads each: 8 sequences of 32768 tokens 92.6 us, 5.8 TB/s (0.88 of the copies'); 4 of up to
-// 131072 126.8 us, 5.8 TB/s; 8 draft tokens of 8 sequences of up to 32768 163 us, 2.3 TB/s, bound by the conversions and
-// softmax of 32 rows; one sequence of 4096 9.5 us, latency.  Three CTAs an SM against two: 110 against 123 us; tiles of 8
-// rows instead of 16 for up to 8: 93 against 107 (8 sequences of 32768).
+// 8 KV heads of 128, 4 query heads each: 8 sequences of 32768 tokens 92 to 96 us from GPU to GPU, 5.6 to 5.8 TB/s (0.85 to
+// 0.88 of the copies'); 4 of up to 131072, int8, 130 to 143 us, 5.1 to 5.6 TB/s; 8 draft tokens of 8 sequences of up to 32768
+// 159 us, 2.3 TB/s, bound by the conversions and softmax of 32 rows; one sequence of 4096 9.4 us, latency.  Three CTAs an SM
+// against two: 110 against 123 us; tiles of 8 rows instead of 16 for up to 8: 93 against 107 (8 sequences of 32768).
 
 constexpr int kMaxCluster = kPagedMaxCluster;
 __device__ __forceinline__ void cluster_sync() {
@@ -803,8 +803,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_tiles_kernel(const Pa
 // one shared ring; every warp converts the codes itself (the conversions run
 // beside the other warps' products).  Few row tiles over a long cache are cut
 // into n_splits parts of their stages, joined by paged_join_rows_kernel.
-// Bound by the conversions and the warps' matrix instructions: 128 tokens of 8192, 32 heads of 128, fp16: 173 us, 99
-// TFLOP/s of the attention's own products (half as much again is done for the weights' second part).
+// Bound by the conversions and the warps' matrix instructions: 32 heads of 128, 128 tokens of 8192 134 us, 127 TFLOP/s of
+// the attention's own products (half as much again is done for the weights' second part); 2047 of 10001 1855 us, 162 TFLOP/s.
 
 constexpr int kWideRing = 4;
 

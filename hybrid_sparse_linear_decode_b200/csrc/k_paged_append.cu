@@ -13,7 +13,7 @@ namespace {
 //
 // Bound by bytes for a prompt, by the chain page table -> row -> scale for a few tokens.  32768 tokens of 32 and 8 heads of
 // 128: 150 us, 5.0 TB/s (of the copies' 6.6); 2 rows a thread 194 us against 171 for 4 when measured.  8 sequences, one
-// token: 2.9 us.  Queries in a launch of their own take longer at all sizes: 2048 tokens 15.0 us against 11.1, 32768 152
+// token: 5.3 us.  Queries in a launch of their own take longer at all sizes: 2048 tokens 15.0 us against 11.1, 32768 152
 // against 150.
 
 constexpr int kAppendRows = 4;  // rows a thread holds

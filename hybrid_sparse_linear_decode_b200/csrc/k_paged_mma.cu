@@ -11,10 +11,10 @@
 // rescaled rarely: weights are 2^(z - m + 7) vs / ref, at most 2^15, with full 11 bits down to 2^-21 of the largest; ref is
 // a row's own, from the scales of what it sees.
 //
-// 2047 tokens of 10001, 32 heads of 128: 606 us, 497 TFLOP/s.  Bound by the chain of a tile: the operands' way from shared
-// memory and the conversions into it (about 2000 clocks a tile) beside a softmax of about 3400.  Tiles of 64 tokens with two
-// accumulators of logits took 722 us when this form took 665: a product of 64 columns reads as many bytes of its left
-// operand as one of 128.  Row tiles unit by unit took 665 us, all units' last ones first 639, the last turn's in parts 606.
+// 2047 tokens of 10001, 32 heads of 128: 580 us, 519 TFLOP/s.  Bound by the chain of a tile: the operands' way from shared
+// memory and the conversions into it (about 2000 clocks a tile) beside a softmax of about 3400 when it took 606 us.  Tiles of
+// 64 tokens with two accumulators of logits took 722 us when this form took 665: a product of 64 columns reads as many bytes of
+// its left operand as one of 128.  Row tiles unit by unit took 665 us, all units' last ones first 639, the last turn's in parts 606.
 #include "k_paged.cuh"
 #include "k_tcgen05.cuh"
 

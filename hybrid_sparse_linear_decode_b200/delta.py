@@ -53,7 +53,8 @@ class GatedDeltaState:
         """Takes a step's tokens through the states in place.  Sequence b owns rows cu[b] .. cu[b + 1] (int32, device) and
         state ``slots[b]`` (int32, device; default b; -1: the sequence is skipped, its rows stay as they were); ``max_new``
         bounds the rows of one sequence.  q, k [rows, n_k_heads, key_dim], v [rows, n_v_heads, value_dim] bf16; g, beta
-        [rows, n_v_heads] fp32.  Returns [rows, n_v_heads, value_dim] bf16."""
+        [rows, n_v_heads] fp32.  Returns [rows, n_v_heads, value_dim] bf16 (``out``, if given, in other memory than the
+        inputs).  Tokens cannot be taken out of a state again: for drafts that may be rejected keep a copy of it."""
         if stream is not None:
             with on_stream(stream, self.device):
                 return self.run(q, k, v, g, beta, cu, max_new, slots, scale, out)

@@ -68,7 +68,8 @@ class PagedKVCache:
                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
         """Append a step's tokens: k, v [rows, n_kv_heads, d] (bf16 or fp16), keys rotated by ``rope`` (fp32
         [positions, rot_dim]: cosines, then sines).  With ``q`` [rows, n_q_heads, d] returns the queries rotated alike
-        (into ``q_out``, which may be ``q``)."""
+        (into ``q_out``, which may be ``q``).  ``stream``: the caller's stream instead of the current one; tensors made on
+        another one have to outlive the call (``record_stream``)."""
         if stream is not None:
             with on_stream(stream, self.device):
                 return self.append(k, v, cu, kv_lens, page_table, max_new, rope, interleaved, q, q_out)
@@ -81,7 +82,8 @@ class PagedKVCache:
         """Causal attention of the step's tokens q [rows, n_q_heads, d] over the cache (append them first): returns out
         [rows, n_q_heads, d] in q's type, with ``return_lse`` also the fp32 [rows, n_q_heads] logarithms of the softmax
         sums.  ``window`` > 0 hides positions t - window and before, but for the first ``n_sink``.  Rows behind
-        the last sequence are left as they were (in new tensors: not written)."""
+        the last sequence are left as they were (in new tensors: not written).  ``out`` is in other memory than q;
+        ``scale`` 0 selects 1/sqrt(d)."""
         if stream is not None:
             with on_stream(stream, self.device):
                 return self.attend(q, cu, kv_lens, page_table, max_new, max_len, window, n_sink, scale, out, return_lse)

@@ -489,7 +489,9 @@ typedef struct hyb_attn_paged_batch {
  * A page that the new tokens begin gets the scale that they need.  A page that
  * already holds tokens of the sequence keeps its scale unless a new token needs a
  * larger one; its codes are then rewritten once for the new scale.  Codes are
- * the nearest (ties to even) to x / scale.  A NaN is stored as 0 and an infinity as the
+ * the nearest (ties to even) to x * (1 / scale), the reciprocal and the product
+ * rounded to 32 bits (for e4m3, whose scales are powers of two, x / scale exactly;
+ * for int8 next to ties either neighbour of x / scale).  A NaN is stored as 0 and an infinity as the
  * largest code, both without effect on the scale, and set
  * HYB_STATUS_NONFINITE.  Appending the same tokens again gives the same cache.
  * A position at or past n_pos takes the last one's angles and sets
@@ -559,6 +561,9 @@ typedef struct hyb_attn_delta_state {
  *          In chunks errors are relative to the largest element of a column of the state
  *          within a chunk, or to 2^-119 where that is larger.
  *   out    bf16 rows of [n_v_heads][value_dim], in other memory than the inputs
+ * The state after a call holds all of its tokens and none can be taken out again: a
+ * caller that verifies draft tokens keeps a copy of the states (or has the drafts run
+ * in slots of their own) and takes the accepted tokens through the kept ones.
  * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
  * the tokens one by one with the state in registers; long ones in chunks of 64
  * by matrix products, where a wait that runs out (about 1 s) sets

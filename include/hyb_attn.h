@@ -522,7 +522,8 @@ size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hy
  * The workspace (16-byte aligned; 0 bytes and NULL where the size is 0) holds
  * nothing between calls; calls that may run at the same time need one each.  A
  * wait inside the kernel that runs out (about 1 s) sets HYB_STATUS_TIMEOUT in
- * the batch's status, and the rows are invalid.  Limits: batch * n_kv_heads <=
+ * the batch's status, and the rows are invalid.  One form serves the whole call, chosen
+ * by max_new: a batch that mixes long runs with many single tokens is faster as two calls.  Limits: batch * n_kv_heads <=
  * 65535.  Errors: HYB_EINVAL, HYB_ESCRATCH (workspace too small), HYB_ECUDA. */
 int hyb_attn_paged_attend(const hyb_attn_paged_cache* cache, const hyb_attn_paged_batch* batch, int32_t type,
                           const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse,
@@ -566,7 +567,8 @@ typedef struct hyb_attn_delta_state {
  * in slots of their own) and takes the accepted tokens through the kept ones.
  * scale 0 selects 1/sqrt(key_dim).  The state stays in 32 bits.  Short runs take
  * the tokens one by one with the state in registers; long ones in chunks of 64
- * by matrix products, where a wait that runs out (about 1 s) sets
+ * by matrix products (all sequences of a call alike, by max_new; a batch that mixes
+ * the two is faster as two calls), where a wait that runs out (about 1 s) sets
  * HYB_STATUS_TIMEOUT and leaves outputs and states invalid.  One launch, no
  * workspace.  Errors: HYB_EINVAL, HYB_ECUDA. */
 int hyb_attn_delta_run(const hyb_attn_delta_state* state, const void* q, int64_t q_stride, const void* k,

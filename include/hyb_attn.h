@@ -516,7 +516,9 @@ size_t hyb_attn_paged_workspace_size(const hyb_attn_paged_cache* cache, const hy
  *   lse    fp32 [n_new][n_q_heads]: log of the sum of exp(scale q . k_j); or NULL
  * A row that sees nothing gets zeros and lse = -inf.  scale 0 selects
  * 1/sqrt(head_dim).  Values are as if in 32 bits but for the softmax weights,
- * which are rounded to 11 bits (bf16 rows) or 22 (fp16 rows).  Scales of visible
+ * which are rounded to 11 bits (bf16 rows) or 22 (fp16 rows), and not finer than
+ * 2^-32 (bf16, more than 32 rows a KV head) or 2^-40 of the largest weight and of
+ * the largest value scale that the row sees.  Scales of visible
  * tokens are finite and not negative, and codes no NaN, as an append leaves them;
  * what lies in pages behind a sequence's end or outside its window is not used.
  * The workspace (16-byte aligned; 0 bytes and NULL where the size is 0) holds
